@@ -10,6 +10,7 @@ the built library raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -22,6 +23,9 @@ __all__ = [
     "falqon_linear_bwd_folded", "folded_t_planes", "falqon_selftest_bounded_waits", "falqon_workspace_init",
     "workspace", "falqon_lora_separate_fwd", "falqon_lora_separate_bwd", "separate_saved_views",
     "separate_bwd_views", "falqon_linear_fwd_grouped",
+    "falqon_norm_fwd", "falqon_norm_bwd", "falqon_linear_fwd_epilogue", "falqon_linear_epilogue_bwd",
+    "falqon_clip_grads", "GradList", "NORM_LAYER", "NORM_RMS", "ACT_NONE", "ACT_RELU", "ACT_GELU_ERF",
+    "ACT_GELU_TANH", "ACT_SILU", "OP_NORM_BWD", "OP_LINEAR_EPILOGUE_BWD", "OP_CLIP_GRADS",
     "SEPARATE_BF16", "SEPARATE_FP8", "OP_QUANTIZE",
     "OP_LINEAR_FWD",
     "OP_LINEAR_BWD", "OP_PROXY_UPDATE", "OP_PROXY_UPDATE_TOPK", "OP_FOLDED_T", "OP_LINEAR_BWD_FOLDED",
@@ -35,7 +39,10 @@ OP_QUANTIZE, OP_LINEAR_FWD, OP_LINEAR_BWD, OP_PROXY_UPDATE, OP_PROXY_UPDATE_TOPK
 OP_FOLDED_T, OP_LINEAR_BWD_FOLDED = 5, 6
 OP_SEPARATE_SAVED_BF16, OP_SEPARATE_SAVED_FP8, OP_SEPARATE_FWD_FP8 = 7, 8, 9
 OP_SEPARATE_BWD_BF16, OP_SEPARATE_BWD_FP8 = 10, 11
+OP_NORM_BWD, OP_LINEAR_EPILOGUE_BWD, OP_CLIP_GRADS = 12, 13, 14
 SEPARATE_BF16, SEPARATE_FP8 = 0, 1
+NORM_LAYER, NORM_RMS = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU_ERF, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 DTYPE_BF16, DTYPE_F32 = 0, 1
 PROXY_ACCUMULATE, PROXY_SELECT, PROXY_KEEP_RESIDUAL, PROXY_STRICT, PROXY_TENSOR = 1, 2, 4, 8, 16
 PROXY_DEFER_CLEAR = 32  # with ACCUMULATE | SELECT: row_mask carries the clear to the next call
@@ -48,7 +55,8 @@ EXPORTED_SYMBOLS = (
     "falqon_linear_bwd_noalloc", "falqon_proxy_update_topk", "falqon_quantize_e5m2",
     "falqon_linear_bwd_e5m2", "falqon_linear_fwd_folded", "falqon_linear_bwd_folded",
     "falqon_selftest_bounded_waits", "falqon_workspace_init", "falqon_lora_separate_fwd",
-    "falqon_lora_separate_bwd", "falqon_linear_fwd_grouped",
+    "falqon_lora_separate_bwd", "falqon_linear_fwd_grouped", "falqon_norm_fwd", "falqon_norm_bwd",
+    "falqon_linear_fwd_epilogue", "falqon_linear_epilogue_bwd", "falqon_clip_grads",
 )
 
 
@@ -93,6 +101,15 @@ def lib():
                                            p, p, p, sz, p]
     L.falqon_linear_fwd_grouped.argtypes = [p, p, C.c_int, p, p, p, p, i64, i64, p, p]
     L.falqon_linear_fwd_grouped.restype = C.c_int
+    f32 = C.c_float
+    L.falqon_norm_fwd.argtypes = [p, C.c_int, p, p, C.c_int, C.c_int, i64, i64, f32, p, p, p, p, p]
+    L.falqon_norm_bwd.argtypes = [p, p, C.c_int, p, C.c_int, C.c_int, p, p, p, i64, i64, p, p, p, p, sz, p]
+    L.falqon_linear_fwd_epilogue.argtypes = [p, p, p, p, p, C.c_int, C.c_int, p, i64, i64, i64, p, p, p, p]
+    L.falqon_linear_epilogue_bwd.argtypes = [p, p, C.c_int, i64, i64, p, p, p, sz, p]
+    L.falqon_clip_grads.argtypes = [C.c_int, p, p, p, f32, f32, p, p, p, p, p, sz, p]
+    for f in ("falqon_norm_fwd", "falqon_norm_bwd", "falqon_linear_fwd_epilogue", "falqon_linear_epilogue_bwd",
+              "falqon_clip_grads"):
+        getattr(L, f).restype = C.c_int
     L.falqon_workspace_init.argtypes = [p, sz, p]
     L.falqon_workspace_init.restype = C.c_int
     L.falqon_workspace_size.argtypes = [C.c_int, i64, i64, i64, i64]
@@ -471,3 +488,220 @@ def falqon_lora_separate_bwd(precision, dyq, s_dy, dy, wq, s_w, xq, s_x, x, A, B
         M, N, K, r, _ptr(dx_t), _ptr(dA_t), _ptr(dB_t), _ptr(dev_status), _ptr(ws), wsb, _stream(stream, dev))
     _check(st, "falqon_lora_separate_bwd")
     return dx_t, dA_t, dB_t
+
+
+# ------------------------------------------------------------------ around the linear layer
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
+def _on(dev, stream):
+    """Makes `dev` and the caller's stream current, where they are not: what is
+    allocated then belongs to the stream that the call runs on."""
+    if stream is not None:
+        return torch.cuda.stream(stream)  # also selects the stream's device
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _expect(t, name, shape, dtypes, dev):
+    """The call reads `shape` elements of `dtypes` on `dev` behind this pointer."""
+    if t is None:
+        return
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+_F32, _BF16, _EITHER = (torch.float32,), (torch.bfloat16,), (torch.bfloat16, torch.float32)
+_CODES = tuple(getattr(torch, n) for n in ("uint8", "float8_e4m3fn"))
+
+
+def _cuda_2d(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if not t.is_cuda:
+        raise ValueError("falqon tensors must live on a CUDA device")
+
+
+def _output(v, name, shape, dtype, dev):
+    """An output that may be True (allocate), a tensor, or None (not wanted)."""
+    if v is True:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if v is None or v is False:
+        return None
+    _expect(v, name, shape, (dtype,), dev)
+    return v
+
+
+def _scratch(op, M, N, K, dev, workspace):
+    """A workspace that needs no initialisation: the caller's, or one of this call."""
+    need = falqon_workspace_size(op, M, N, K, 0)
+    if workspace is None:
+        raw = torch.empty(need + 256, dtype=torch.uint8, device=dev)
+        off = (-raw.data_ptr()) % 256
+        return raw[off:off + need], need
+    if workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def falqon_norm_fwd(x, gamma=None, beta=None, eps=1e-5, kind=NORM_LAYER, y=True, mean=True, rstd=True,
+                    dev_status=None, stream=None):
+    """Layer norm (or RMS norm: kind=NORM_RMS, no beta) of each row of x [rows,
+    cols], bf16 or fp32; returns (y, mean, rstd).  mean and rstd (float32
+    [rows], what falqon_norm_bwd reads) may be True (allocate), a tensor, or
+    None; mean is None for NORM_RMS."""
+    _cuda_2d(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float32")
+    _expect(gamma, "gamma", (cols,), _EITHER, dev)
+    _expect(beta, "beta", (cols,), _EITHER if gamma is None else (gamma.dtype,), dev)
+    param = gamma if gamma is not None else beta
+    with _on(dev, stream):
+        y = _output(True if y is None else y, "y", x.shape, x.dtype, dev)
+        mean = _output(None if kind == NORM_RMS and mean is True else mean, "mean", (rows,), torch.float32, dev)
+        rstd = _output(rstd, "rstd", (rows,), torch.float32, dev)
+        st = lib().falqon_norm_fwd(_ptr(x), _DTYPES[x.dtype], _ptr(gamma), _ptr(beta),
+                                   DTYPE_BF16 if param is None else _DTYPES[param.dtype], int(kind), rows, cols,
+                                   float(eps), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(dev_status),
+                                   _stream(stream, dev))
+    _check(st, "falqon_norm_fwd")
+    return y, mean, rstd
+
+
+def falqon_norm_bwd(dy, x, gamma, mean, rstd, kind=NORM_LAYER, dres=None, dx=True, dgamma=True, dbeta=True,
+                    workspace=None, stream=None):
+    """Backward of falqon_norm_fwd; dres (nullable) joins dx.  Each output may
+    be True (allocate), a tensor, or None; dgamma and dbeta are float32 sums,
+    dbeta is None for NORM_RMS.  Returns (dx, dgamma, dbeta)."""
+    _cuda_2d(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    if x.dtype not in _DTYPES:
+        raise ValueError("x must be bfloat16 or float32")
+    _expect(dy, "dy", x.shape, (x.dtype,), dev)
+    _expect(dres, "dres", x.shape, (x.dtype,), dev)
+    _expect(gamma, "gamma", (cols,), _EITHER, dev)
+    _expect(mean, "mean", (rows,), _F32, dev)
+    _expect(rstd, "rstd", (rows,), _F32, dev)
+    with _on(dev, stream):
+        dx = _output(dx, "dx", x.shape, x.dtype, dev)
+        dgamma = _output(dgamma, "dgamma", (cols,), torch.float32, dev)
+        dbeta = _output(None if kind == NORM_RMS and dbeta is True else dbeta, "dbeta", (cols,), torch.float32, dev)
+        ws, wsb = (None, 0)
+        if dgamma is not None or dbeta is not None:
+            ws, wsb = _scratch(OP_NORM_BWD, rows, 0, cols, dev, workspace)
+        st = lib().falqon_norm_bwd(_ptr(dy), _ptr(x), _DTYPES[x.dtype], _ptr(gamma),
+                                   DTYPE_BF16 if gamma is None else _DTYPES[gamma.dtype], int(kind), _ptr(mean),
+                                   _ptr(rstd), _ptr(dres), rows, cols, _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+                                   _ptr(ws), wsb, _stream(stream, dev))
+    _check(st, "falqon_norm_bwd")
+    return dx, dgamma, dbeta
+
+
+def falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias=None, act=ACT_NONE, residual=None, z=None, y=True,
+                               dev_status=None, stream=None):
+    """Y = act(Xq . Wq^T / (s_x s_w) + bias) + residual in bf16; returns (y, z).
+    z, the pre-activation in bf16 for falqon_linear_epilogue_bwd, may be True
+    (allocate), a tensor, or None."""
+    _cuda_2d(xq, "xq")
+    _cuda_2d(wq, "wq")
+    M, K = xq.shape
+    N = wq.shape[0]
+    dev = xq.device
+    _expect(xq, "xq", (M, K), _CODES, dev)
+    _expect(wq, "wq", (N, K), _CODES, dev)
+    for t, name in ((s_x, "s_x"), (s_w, "s_w")):
+        _expect(t, name, t.shape if t.numel() == 1 else (1,), _F32, dev)
+    _expect(bias, "bias", (N,), _EITHER, dev)
+    _expect(residual, "residual", (M, N), _BF16, dev)
+    with _on(dev, stream):
+        y = _output(True if y is None else y, "y", (M, N), torch.bfloat16, dev)
+        z = _output(z, "z", (M, N), torch.bfloat16, dev)
+        st = lib().falqon_linear_fwd_epilogue(
+            _ptr(_u8(xq)), _ptr(s_x), _ptr(_u8(wq)), _ptr(s_w), _ptr(bias),
+            DTYPE_BF16 if bias is None else _DTYPES[bias.dtype], int(act), _ptr(residual), M, N, K, _ptr(z), _ptr(y),
+            _ptr(dev_status), _stream(stream, dev))
+    _check(st, "falqon_linear_fwd_epilogue")
+    return y, z
+
+
+def falqon_linear_epilogue_bwd(dy, z, act, dz=True, dbias=True, workspace=None, stream=None):
+    """dZ = dY act'(Z) in bf16 and dbias, its column sums in float32; each may
+    be True (allocate), a tensor, or None.  z may be None for ACT_NONE, whose
+    dZ is dY.  Returns (dz, dbias)."""
+    _cuda_2d(dy, "dy")
+    M, N = dy.shape
+    dev = dy.device
+    _expect(dy, "dy", (M, N), _BF16, dev)
+    _expect(z, "z", (M, N), _BF16, dev)
+    with _on(dev, stream):
+        dz = _output(dz, "dz", (M, N), torch.bfloat16, dev)
+        dbias = _output(dbias, "dbias", (N,), torch.float32, dev)
+        ws, wsb = (None, 0)
+        if dbias is not None:
+            ws, wsb = _scratch(OP_LINEAR_EPILOGUE_BWD, M, N, 0, dev, workspace)
+        st = lib().falqon_linear_epilogue_bwd(_ptr(dy), _ptr(z), int(act), M, N, _ptr(dz), _ptr(dbias), _ptr(ws), wsb,
+                                              _stream(stream, dev))
+    _check(st, "falqon_linear_epilogue_bwd")
+    return dz, dbias
+
+
+class GradList:
+    """Tensors (bf16 or float32, contiguous, on one device) marshalled once for
+    falqon_clip_grads: a training loop whose gradient buffers stay where they
+    are builds it at its start.  Keeps the tensors alive."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.device = self.tensors[0].device
+        for t in self.tensors:
+            if t.dtype not in _DTYPES:
+                raise ValueError(f"gradients must be bfloat16 or float32, got {t.dtype}")
+            if t.device != self.device:
+                raise ValueError(f"gradients on {self.device} and {t.device}")
+        n = len(self.tensors)
+        self.pointers = (C.c_void_p * n)(*[_ptr(t) for t in self.tensors])
+        self.numel = (C.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self.dtypes = (C.c_int * n)(*[_DTYPES[t.dtype] for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+    def __iter__(self):
+        return iter(self.tensors)
+
+
+def falqon_clip_grads(grads, max_norm, factor=1.0, out=None, norm=None, coef=None, dev_status=None, workspace=None,
+                      stream=None):
+    """The global norm of `grads` (tensors, or a GradList of them), and, where
+    `out` is wanted, the gradients times factor * min(1, max_norm / norm).
+    out: None (the norm alone), True (allocate), or tensors / a GradList of the
+    same sizes and types, which may be `grads` itself (in place).  Returns
+    (out, norm, coef), norm and coef being float32 [1]."""
+    g = grads if isinstance(grads, GradList) else GradList(grads)
+    dev = g.device
+    with _on(dev, stream):
+        o = out
+        if out is True:
+            o = GradList(torch.empty_like(t) for t in g)
+        elif out is not None and not isinstance(out, GradList):
+            o = GradList(out)
+        if o is not None and o is not g:
+            if len(o) != len(g) or o.device != dev or bytes(o.numel) != bytes(g.numel) or \
+                    bytes(o.dtypes) != bytes(g.dtypes):
+                raise ValueError("out must match grads in number, sizes, types and device")
+        norm = _output(True if norm is None else norm, "norm", (1,), torch.float32, dev)
+        coef = _output(True if coef is None else coef, "coef", (1,), torch.float32, dev)
+        ws, wsb = _scratch(OP_CLIP_GRADS, 0, 0, 0, dev, workspace)
+        st = lib().falqon_clip_grads(len(g), g.pointers, g.dtypes, g.numel, float(max_norm), float(factor),
+                                     None if o is None else o.pointers, _ptr(norm), _ptr(coef), _ptr(dev_status),
+                                     _ptr(ws), wsb, _stream(stream, dev))
+    _check(st, "falqon_clip_grads")
+    return (None if o is None else o.tensors), norm, coef

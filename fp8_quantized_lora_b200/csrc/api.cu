@@ -1,5 +1,9 @@
 // C ABI of libfalqon: argument validation, workspace layout, dispatch.
+#include <algorithm>
+#include <cmath>
+#include <memory>
 #include <mutex>
+#include <new>
 
 #include "../../include/falqon.h"
 #include "internal.h"
@@ -169,6 +173,13 @@ size_t falqon_workspace_size(falqon_op op, int64_t M, int64_t N, int64_t K, int6
     case FALQON_OP_SEPARATE_BWD_FP8:
       if (M <= 0 || N <= 0 || K <= 0 || r <= 0) return 0;
       return separate_bwd_workspace_bytes(op == FALQON_OP_SEPARATE_BWD_FP8, M, N, K, r);
+    case FALQON_OP_NORM_BWD:
+      if (M <= 0 || K <= 0) return 0;
+      return norm_bwd_workspace_bytes(M, K);
+    case FALQON_OP_LINEAR_EPILOGUE_BWD:
+      if (M <= 0 || N <= 0) return 0;
+      return epilogue_bwd_workspace_bytes(M, N);
+    case FALQON_OP_CLIP_GRADS: return clip_workspace_bytes();
   }
   return 0;
 }
@@ -507,6 +518,167 @@ falqon_status falqon_linear_fwd_grouped(const uint8_t* xq, const float* s_x, int
   if (!current_device_info()) return FALQON_ERR_CUDA;
   return from_cuda(launch_fp8_gemm_fwd_grouped(xq, s_x, nseg, wq, s_w, N, y, M, K, dev_status,
                                                static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- around the linear layer
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 256;
+
+bool known_dtype(falqon_dtype d) { return d == FALQON_DTYPE_BF16 || d == FALQON_DTYPE_F32; }
+bool known_act(falqon_act a) { return a >= FALQON_ACT_NONE && a <= FALQON_ACT_SILU; }
+bool unaligned16(const void* p) { return !aligned16(p); }  // null counts as aligned
+
+falqon_status norm_shape(falqon_dtype dtype, falqon_dtype param_dtype, falqon_norm kind, int64_t rows, int64_t cols) {
+  if (!known_dtype(dtype) || !known_dtype(param_dtype)) return FALQON_ERR_INVALID_ARG;
+  if (kind != FALQON_NORM_LAYER && kind != FALQON_NORM_RMS) return FALQON_ERR_INVALID_ARG;
+  if (rows <= 0 || cols <= 0) return FALQON_ERR_INVALID_ARG;
+  if (rows > kMaxDim || cols > kMaxDim) return FALQON_ERR_UNSUPPORTED;
+  return FALQON_OK;
+}
+
+// A tensor's bytes in memory, for the overlap checks of falqon_clip_grads.
+struct Span {
+  uintptr_t begin, end;
+  int index;
+  bool operator<(const Span& o) const { return begin < o.begin; }
+};
+
+size_t grad_bytes(falqon_dtype d, int64_t numel) {
+  return static_cast<size_t>(numel) * (d == FALQON_DTYPE_BF16 ? 2 : 4);
+}
+
+// Outputs may not overlap one another, nor any gradient but their own, which
+// they then equal (in place).
+falqon_status clip_overlaps(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                            void* const* outs) {
+  std::unique_ptr<Span[]> span(new (std::nothrow) Span[n]);
+  if (!span) return FALQON_ERR_UNSUPPORTED;
+  int k = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(outs[i]);
+    span[k++] = Span{b, b + grad_bytes(dtypes[i], numel[i]), i};
+  }
+  std::sort(span.get(), span.get() + k);
+  for (int i = 1; i < k; ++i)
+    if (span[i].begin < span[i - 1].end) return FALQON_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const uintptr_t b = reinterpret_cast<uintptr_t>(grads[i]), e = b + grad_bytes(dtypes[i], numel[i]);
+    // the outputs are disjoint: those that meet [b, e) end with the last one that begins before e
+    const Span* s = std::lower_bound(span.get(), span.get() + k, Span{e, 0, 0});
+    if (s == span.get()) continue;
+    --s;
+    if (s->end <= b) continue;
+    if (s->index != i || s->begin != b) return FALQON_ERR_INVALID_ARG;
+  }
+  return FALQON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+falqon_status falqon_norm_fwd(const void* x, falqon_dtype dtype, const void* gamma, const void* beta,
+                              falqon_dtype param_dtype, falqon_norm kind, int64_t rows, int64_t cols, float eps,
+                              void* y, float* mean, float* rstd, int32_t* dev_status, void* stream) {
+  if (!x || !y) return FALQON_ERR_INVALID_ARG;
+  falqon_status s = norm_shape(dtype, param_dtype, kind, rows, cols);
+  if (s != FALQON_OK) return s;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return FALQON_ERR_INVALID_ARG;
+  if (kind == FALQON_NORM_RMS && (beta || mean)) return FALQON_ERR_INVALID_ARG;
+  if (unaligned16(x) || unaligned16(y) || unaligned16(gamma) || unaligned16(beta) || unaligned16(mean) ||
+      unaligned16(rstd))
+    return FALQON_ERR_UNSUPPORTED;
+  if (!current_device_info()) return FALQON_ERR_CUDA;
+  return from_cuda(launch_norm_fwd(x, dtype == FALQON_DTYPE_BF16, gamma, beta, param_dtype == FALQON_DTYPE_BF16,
+                                   kind == FALQON_NORM_RMS, rows, cols, eps, y, mean, rstd, dev_status,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_dtype dtype, const void* gamma,
+                              falqon_dtype param_dtype, falqon_norm kind, const float* mean, const float* rstd,
+                              const void* dres, int64_t rows, int64_t cols, void* dx, float* dgamma, float* dbeta,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dx && !dgamma && !dbeta) return FALQON_ERR_INVALID_ARG;
+  if (!dy || !x || !rstd) return FALQON_ERR_INVALID_ARG;
+  falqon_status s = norm_shape(dtype, param_dtype, kind, rows, cols);
+  if (s != FALQON_OK) return s;
+  if (kind == FALQON_NORM_LAYER ? !mean : (mean || dbeta)) return FALQON_ERR_INVALID_ARG;
+  if (dres && !dx) return FALQON_ERR_INVALID_ARG;
+  if (unaligned16(dy) || unaligned16(x) || unaligned16(gamma) || unaligned16(mean) || unaligned16(rstd) ||
+      unaligned16(dres) || unaligned16(dx) || unaligned16(dgamma) || unaligned16(dbeta))
+    return FALQON_ERR_UNSUPPORTED;
+  if (dgamma || dbeta) {
+    s = check_ws(norm_bwd_workspace_bytes(rows, cols), workspace, workspace_bytes);
+    if (s != FALQON_OK) return s;
+  }
+  if (!current_device_info()) return FALQON_ERR_CUDA;
+  return from_cuda(launch_norm_bwd(dy, x, dtype == FALQON_DTYPE_BF16, gamma, param_dtype == FALQON_DTYPE_BF16,
+                                   kind == FALQON_NORM_RMS, mean, rstd, dres, rows, cols, dx, dgamma, dbeta,
+                                   workspace, static_cast<cudaStream_t>(stream)));
+}
+
+falqon_status falqon_linear_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                                         const void* bias, falqon_dtype bias_dtype, falqon_act act,
+                                         const void* residual, int64_t M, int64_t N, int64_t K, void* z, void* y,
+                                         int32_t* dev_status, void* stream) {
+  if (!xq || !s_x || !wq || !s_w || !y) return FALQON_ERR_INVALID_ARG;
+  if (M <= 0 || N <= 0 || K <= 0) return FALQON_ERR_INVALID_ARG;
+  if (!known_act(act) || (bias && !known_dtype(bias_dtype))) return FALQON_ERR_INVALID_ARG;
+  if (N % 16 != 0 || K % 16 != 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return FALQON_ERR_UNSUPPORTED;
+  if (unaligned16(xq) || unaligned16(wq) || unaligned16(y) || unaligned16(bias) || unaligned16(residual) ||
+      unaligned16(z))
+    return FALQON_ERR_UNSUPPORTED;
+  if (!current_device_info()) return FALQON_ERR_CUDA;
+  const LinearEpilogue epi{bias, bias_dtype == FALQON_DTYPE_BF16, act, residual, z};
+  return from_cuda(launch_fp8_gemm_fwd_epilogue(xq, s_x, wq, s_w, M, N, K, epi, y, dev_status,
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+falqon_status falqon_linear_epilogue_bwd(const void* dy, const void* z, falqon_act act, int64_t M, int64_t N,
+                                         void* dz, float* dbias, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+  if (!dz && !dbias) return FALQON_ERR_INVALID_ARG;
+  if (!dy || M <= 0 || N <= 0 || !known_act(act)) return FALQON_ERR_INVALID_ARG;
+  if (act != FALQON_ACT_NONE && !z) return FALQON_ERR_INVALID_ARG;
+  if (N % 16 != 0 || M > kMaxDim || N > kMaxDim) return FALQON_ERR_UNSUPPORTED;
+  if (unaligned16(dy) || unaligned16(z) || unaligned16(dz) || unaligned16(dbias)) return FALQON_ERR_UNSUPPORTED;
+  if (dbias) {
+    falqon_status s = check_ws(epilogue_bwd_workspace_bytes(M, N), workspace, workspace_bytes);
+    if (s != FALQON_OK) return s;
+  }
+  if (!current_device_info()) return FALQON_ERR_CUDA;
+  return from_cuda(launch_epilogue_bwd(dy, z, act, M, N, dz, dbias, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+falqon_status falqon_clip_grads(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                                float max_norm, float factor, void* const* outs, float* norm, float* coef,
+                                int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream) {
+  if (n <= 0 || !grads || !dtypes || !numel || !norm) return FALQON_ERR_INVALID_ARG;
+  if (!(max_norm > 0.0f) || !std::isfinite(factor)) return FALQON_ERR_INVALID_ARG;
+  int64_t chunks = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] < 0 || !known_dtype(dtypes[i])) return FALQON_ERR_INVALID_ARG;
+    if (numel[i] == 0) continue;
+    if (!grads[i] || (outs && !outs[i])) return FALQON_ERR_INVALID_ARG;
+    if (unaligned16(grads[i]) || (outs && unaligned16(outs[i]))) return FALQON_ERR_UNSUPPORTED;
+    if (numel[i] > (int64_t(1) << 42)) return FALQON_ERR_UNSUPPORTED;
+    chunks += numel[i] / clip_chunk_elements() + 1;
+    if (chunks > INT32_MAX) return FALQON_ERR_UNSUPPORTED;
+  }
+  if (outs) {
+    falqon_status s = clip_overlaps(n, grads, dtypes, numel, outs);
+    if (s != FALQON_OK) return s;
+  }
+  falqon_status s = check_ws(clip_workspace_bytes(), workspace, workspace_bytes);
+  if (s != FALQON_OK) return s;
+  if (!current_device_info()) return FALQON_ERR_CUDA;
+  return from_cuda(launch_clip_grads(n, grads, dtypes, numel, max_norm, factor, outs, norm, coef, dev_status,
+                                     workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

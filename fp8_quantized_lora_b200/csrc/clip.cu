@@ -1,0 +1,204 @@
+// The global norm of many gradient tensors, and clipping by it.
+//
+//   norm = sqrt(sum of g^2 over every element of every tensor)
+//   coef = max_norm / norm where norm > max_norm, else 1
+//   out  = g (factor coef), rounded once to g's type
+//
+// Bound by HBM: every gradient is read for the norm, read again for the
+// scaling and written.  The tensors are cut into chunks of 4096 elements that
+// the blocks take in turn; a table of the tensors travels in the kernel's
+// parameters, so a call copies nothing to the device and can be captured.
+//
+// Sums: eight (bf16) or four (float32) squares are added in float32, which is
+// exact enough while the sum stays away from the ends of float32's range, and
+// in float64 otherwise; everything above one 16-byte vector is float64.  So
+// neither gradients near 1e-30 nor near 1e30 spoil the norm.  The blocks'
+// sums are joined in a fixed order: the result does not depend on the
+// schedule.
+#include "elem.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace falqon {
+namespace {
+
+constexpr int kClipThreads = 256;
+constexpr int kClipChunk = 4096;    // elements
+constexpr int kClipTensors = 512;   // tensors of one launch
+constexpr int kClipBlocks = 592;    // four per SM of a B200
+
+struct ClipTable {
+  const void* in[kClipTensors];
+  void* out[kClipTensors];
+  int64_t numel[kClipTensors];
+  uint32_t end[kClipTensors];      // chunks up to and including tensor i
+  uint8_t bf16[kClipTensors];
+  int32_t n;
+  uint32_t chunks;
+};
+static_assert(sizeof(ClipTable) <= 32000, "kernel parameters");
+
+// The tensor that chunk c belongs to: the first whose end is past c.
+__device__ __forceinline__ int clip_tensor(const ClipTable& t, uint32_t c) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (t.end[mid] > c) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Sum of the squares of one vector: float32 while the sum is in
+// [2^-60, 2^120] (a square below 2^-126 is then nothing beside it, and none
+// overflowed), else float64.
+template <int kN>
+__device__ __forceinline__ double square_sum(const float (&v)[kN]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kN; ++j) s = fmaf(v[j], v[j], s);
+  if (s >= 8.673617e-19f && s <= 1.329228e36f) return static_cast<double>(s);
+  double d = 0.0;
+#pragma unroll
+  for (int j = 0; j < kN; ++j) d = fma(static_cast<double>(v[j]), static_cast<double>(v[j]), d);
+  return d;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ double chunk_square_sum(const void* p, int64_t e0, int64_t e1) {
+  constexpr int kV = kVec<kBF16>;
+  double acc = 0.0;
+  const int64_t whole = e0 + (e1 - e0) / kV * kV;
+  for (int64_t e = e0 + threadIdx.x * kV; e < whole; e += kClipThreads * kV) {
+    float v[kV];
+    unpack16<kBF16>(*reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + e * (16 / kV)), v);
+    acc += square_sum(v);
+  }
+  if (whole + threadIdx.x < e1) {
+    const double v = load_elem<kBF16>(p, whole + threadIdx.x);
+    acc = fma(v, v, acc);
+  }
+  return acc;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void scale_chunk(const void* p, void* o, int64_t e0, int64_t e1, float by, bool zero) {
+  constexpr int kV = kVec<kBF16>;
+  const int64_t whole = e0 + (e1 - e0) / kV * kV;
+  for (int64_t e = e0 + threadIdx.x * kV; e < whole; e += kClipThreads * kV) {
+    float v[kV];
+    unpack16<kBF16>(*reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + e * (16 / kV)), v);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] = zero ? 0.0f : v[j] * by;
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(o) + e * (16 / kV)) = pack16<kBF16>(v);
+  }
+  const int64_t e = whole + threadIdx.x;
+  if (e < e1) store_elem<kBF16>(o, e, zero ? 0.0f : load_elem<kBF16>(p, e) * by);
+}
+
+// part[b] = this block's share (added to what an earlier launch of the call
+// left there when `add`).
+__global__ void __launch_bounds__(kClipThreads)
+    clip_norm_kernel(const __grid_constant__ ClipTable t, double* __restrict__ part, bool add) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[32];
+  double acc = 0.0;
+  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int i = clip_tensor(t, c);
+    const int64_t e0 = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * kClipChunk;
+    const int64_t e1 = e0 + kClipChunk < t.numel[i] ? e0 + kClipChunk : t.numel[i];
+    acc += t.bf16[i] ? chunk_square_sum<true>(t.in[i], e0, e1) : chunk_square_sum<false>(t.in[i], e0, e1);
+  }
+  acc = block_sum(acc, red);
+  if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + acc : acc;
+}
+
+// Every block joins the partial sums (in the same order) and scales its
+// chunks; block 0 of the call's first launch publishes the results.
+__global__ void __launch_bounds__(kClipThreads)
+    clip_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict__ part, int parts,
+                      float max_norm, float factor, bool scale, float* __restrict__ norm, float* __restrict__ coef,
+                      int32_t* __restrict__ dev_status) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double red[32];
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < parts; i += kClipThreads) acc += part[i];
+  acc = block_sum(acc, red);
+  const bool finite = isfinite(acc);  // squares of finite float32 values cannot overflow float64 sums
+  const double n = sqrt(acc);
+  const double c = !finite ? 0.0 : (n > static_cast<double>(max_norm) ? static_cast<double>(max_norm) / n : 1.0);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && norm) {
+    *norm = static_cast<float>(n);
+    if (coef) *coef = static_cast<float>(c);
+    if (!finite && dev_status) atomicOr(dev_status, kDevNonfinite);
+  }
+  if (!scale) return;
+  const float by = static_cast<float>(static_cast<double>(factor) * c);
+  for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const int i = clip_tensor(t, k);
+    const int64_t e0 = static_cast<int64_t>(k - (i ? t.end[i - 1] : 0u)) * kClipChunk;
+    const int64_t e1 = e0 + kClipChunk < t.numel[i] ? e0 + kClipChunk : t.numel[i];
+    if (t.bf16[i]) scale_chunk<true>(t.in[i], t.out[i], e0, e1, by, !finite);
+    else scale_chunk<false>(t.in[i], t.out[i], e0, e1, by, !finite);
+  }
+}
+
+// Fills `t` from tensor `i` on; returns the next tensor.  A launch takes up to
+// kClipTensors tensors that hold elements.
+int clip_table(ClipTable& t, int i, int n, const void* const* grads, void* const* outs, const falqon_dtype* dtypes,
+               const int64_t* numel) {
+  t.n = 0;
+  t.chunks = 0;
+  for (; i < n && t.n < kClipTensors; ++i) {
+    if (numel[i] == 0) continue;
+    t.in[t.n] = grads[i];
+    t.out[t.n] = outs ? outs[i] : nullptr;
+    t.numel[t.n] = numel[i];
+    t.bf16[t.n] = dtypes[i] == FALQON_DTYPE_BF16;
+    t.chunks += static_cast<uint32_t>((numel[i] + kClipChunk - 1) / kClipChunk);
+    t.end[t.n] = t.chunks;
+    ++t.n;
+  }
+  return i;
+}
+
+unsigned clip_grid(const ClipTable& t) {
+  return t.chunks < static_cast<uint32_t>(kClipBlocks) ? (t.chunks ? t.chunks : 1u) : kClipBlocks;
+}
+
+}  // namespace
+
+int64_t clip_chunk_elements() { return kClipChunk; }
+
+size_t clip_workspace_bytes() { return align_up(kClipBlocks * sizeof(double), 256); }
+
+cudaError_t launch_clip_grads(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                              float max_norm, float factor, void* const* outs, float* norm, float* coef,
+                              int32_t* dev_status, void* workspace, cudaStream_t stream) {
+  double* part = static_cast<double*>(workspace);
+  ClipTable t;
+  int parts = 0;
+  for (int i = 0; i < n || parts == 0;) {  // at least one launch: no elements at all give norm 0
+    i = clip_table(t, i, n, grads, outs, dtypes, numel);
+    // the first launch sets how many sums there are; later ones add to them
+    const unsigned grid = parts ? static_cast<unsigned>(parts) : (i < n ? kClipBlocks : clip_grid(t));
+    cudaError_t e = launch_pdl(clip_norm_kernel, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts != 0);
+    if (e != cudaSuccess) return e;
+    parts = static_cast<int>(grid);
+  }
+  bool first = true;
+  for (int i = 0; i < n || first;) {
+    i = clip_table(t, i, n, grads, outs, dtypes, numel);
+    const unsigned grid = outs ? clip_grid(t) : 1u;
+    cudaError_t e = launch_pdl(clip_scale_kernel, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts,
+                               max_norm, factor, outs != nullptr, first ? norm : nullptr, coef, dev_status);
+    if (e != cudaSuccess) return e;
+    first = false;
+    if (!outs) break;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace falqon

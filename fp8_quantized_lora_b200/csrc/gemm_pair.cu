@@ -34,8 +34,14 @@
 // (N = 128 pair MMAs, 64 columns of B per CTA).  An MN-major half is 64
 // bytes wide, so it is staged with the 64-byte swizzle (8-row x 64-byte
 // atoms) and described to the MMA as such.
+//
+// kEpi: the forward with a bias, an activation, a residual and a kept
+// pre-activation in its epilogue (falqon_linear_fwd_epilogue); the plain
+// products are compiled without that code.
 #include <algorithm>
 
+#include "act.cuh"
+#include "elem.cuh"
 #include "internal.h"
 #include "tc_common.cuh"
 
@@ -53,7 +59,57 @@ struct PairArgs {
   const float* scale_a;
   const float* scale_b;
   int32_t* dev_status;
+  LinearEpilogue epi;      // kEpi only; z and residual are [M][ldo] as out
 };
+
+// Eight consecutive elements of the bias as float32.
+__device__ __forceinline__ void load_bias8(const LinearEpilogue& e, int64_t col, float (&b)[8]) {
+  if (e.bias_bf16) {
+    unpack16<true>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + col)), b);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + col);
+    const float4 lo = __ldg(p), hi = __ldg(p + 1);
+    b[0] = lo.x; b[1] = lo.y; b[2] = lo.z; b[3] = lo.w;
+    b[4] = hi.x; b[5] = hi.y; b[6] = hi.z; b[7] = hi.w;
+  }
+}
+
+template <int kAct>
+__device__ __forceinline__ void act8(float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = act_value<kAct>(v[j]);
+}
+
+__device__ __forceinline__ void act8(falqon_act act, float (&v)[8]) {
+  switch (act) {
+    case FALQON_ACT_RELU: act8<FALQON_ACT_RELU>(v); break;
+    case FALQON_ACT_GELU_ERF: act8<FALQON_ACT_GELU_ERF>(v); break;
+    case FALQON_ACT_GELU_TANH: act8<FALQON_ACT_GELU_TANH>(v); break;
+    case FALQON_ACT_SILU: act8<FALQON_ACT_SILU>(v); break;
+    default: break;
+  }
+}
+
+// Eight scaled accumulators through the epilogue: bias, z, activation,
+// residual, one rounding to bf16.  `at`: element offset of the first one.
+__device__ __forceinline__ void store_epilogue8(const LinearEpilogue& e, void* out, int64_t at, int64_t col,
+                                                float (&v)[8]) {
+  if (e.bias) {
+    float b[8];
+    load_bias8(e, col, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += b[j];
+  }
+  if (e.z) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.z) + at) = pack16<true>(v);
+  act8(e.act, v);
+  if (e.residual) {
+    float r[8];
+    unpack16<true>(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.residual) + at), r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+  }
+  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) = pack16<true>(v);
+}
 
 template <bool kBMn, uint32_t kAFmt, int kStages>
 struct PairCfg {
@@ -78,7 +134,7 @@ struct PairCfg {
   static_assert(SmemBytes <= 232448, "shared memory per CTA");
 };
 
-template <class C>
+template <class C, bool kEpi>
 __global__ void __launch_bounds__(C::Threads, 1)
     tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmBh, const PairArgs g) {
@@ -279,7 +335,12 @@ __global__ void __launch_bounds__(C::Threads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int64_t col = col_base + c * 32 + 8 * j;
-            if (col < g.N) {  // N % 8 == 0: eight columns in or out together
+            if (kEpi && col < g.N) {
+              float v[8];
+#pragma unroll
+              for (int h = 0; h < 8; ++h) v[h] = __uint_as_float(r[8 * j + h]) * alpha;
+              store_epilogue8(g.epi, g.out, row * g.ldo + col, col, v);
+            } else if (!kEpi && col < g.N) {  // N % 8 == 0: eight columns in or out together
               uint32_t pk[4];
 #pragma unroll
               for (int h = 0; h < 4; ++h) {
@@ -315,7 +376,7 @@ using PairDxE5Cfg = PairCfg<true, 1u, 6>;  // dYq in E5M2
 
 // Pairs the device can keep resident at once (cached per device): the grid
 // never exceeds it, so the persistent pairs all run in one wave.
-template <class C>
+template <class C, bool kEpi>
 int resident_pairs(const DeviceInfo* di) {
   static int cached[32] = {0};
   const int dev = di->device;
@@ -332,7 +393,7 @@ int resident_pairs(const DeviceInfo* di) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_pair_kernel<C>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_pair_kernel<C, kEpi>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = di->sm_count / 2;
   }
@@ -341,15 +402,16 @@ int resident_pairs(const DeviceInfo* di) {
   return n;
 }
 
-template <class C>
+template <class C, bool kEpi = false>
 cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int64_t M,
-                      int64_t Ncols, int64_t Kc, void* out, int32_t* dev_status, cudaStream_t stream) {
+                      int64_t Ncols, int64_t Kc, void* out, int32_t* dev_status, cudaStream_t stream,
+                      const LinearEpilogue& epi = {}) {
   const DeviceInfo* di = current_device_info();
   if (!di) return cudaErrorInvalidDevice;
   static int configured_mask = 0;  // one bit per device ordinal < 31
   const int bit = di->device < 31 ? (1 << di->device) : 0;
   if (!bit || !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(tc_gemm_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(tc_gemm_pair_kernel<C, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SmemBytes);
     if (e != cudaSuccess) return e;
     if (bit) __atomic_fetch_or(&configured_mask, bit, __ATOMIC_ACQ_REL);
@@ -377,9 +439,10 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
   g.scale_a = sa;
   g.scale_b = sb;
   g.dev_status = dev_status;
+  g.epi = epi;
   const int tiles = g.m_tiles * g.n_tiles;
   if (tiles == 0) return cudaSuccess;
-  const int slots = resident_pairs<C>(di);
+  const int slots = resident_pairs<C, kEpi>(di);
   const int pairs = tiles < slots ? tiles : slots;
   // a partial last wave of at most half the pairs runs as 256 x 128 halves
   const int tail = tiles % pairs;
@@ -389,7 +452,7 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
     g.n_full = tiles - tail;
     g.n_half = 2 * tail;
   }
-  return launch_pdl(tc_gemm_pair_kernel<C>, dim3(static_cast<unsigned>(2 * pairs)), dim3(C::Threads), C::SmemBytes,
+  return launch_pdl(tc_gemm_pair_kernel<C, kEpi>, dim3(static_cast<unsigned>(2 * pairs)), dim3(C::Threads), C::SmemBytes,
                     stream, 2u, tA, tB, tBh, g);
 }
 
@@ -399,6 +462,12 @@ cudaError_t launch_fp8_gemm_fwd_pair(const uint8_t* xq, const float* s_x, const 
                                      int64_t M, int64_t N, int64_t K, void* y, int32_t* dev_status,
                                      cudaStream_t stream) {
   return pair_gemm<PairFwdCfg>(xq, s_x, wq, s_w, M, N, K, y, dev_status, stream);
+}
+
+cudaError_t launch_fp8_gemm_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                                         int64_t M, int64_t N, int64_t K, const LinearEpilogue& epi, void* y,
+                                         int32_t* dev_status, cudaStream_t stream) {
+  return pair_gemm<PairFwdCfg, true>(xq, s_x, wq, s_w, M, N, K, y, dev_status, stream, epi);
 }
 
 cudaError_t launch_fp8_gemm_dx_pair(const uint8_t* dyq, const float* s_dy, const uint8_t* wq, const float* s_w,

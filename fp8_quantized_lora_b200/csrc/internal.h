@@ -195,4 +195,40 @@ cudaError_t launch_proxy_update_topk(uint8_t* wq, const float* s_w, float* Q, co
                                      uint32_t flags, uint8_t* comp_mask, int32_t* n_selected,
                                      int32_t* dev_status, void* workspace, cudaStream_t stream);
 
+// ---------------------------------------------------------------- around the linear layer
+// Layer / RMS norm over the rows of [rows, cols] (norm.cu).
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_norm_fwd(const void* x, bool bf16, const void* gamma, const void* beta, bool param_bf16, bool rms,
+                            int64_t rows, int64_t cols, float eps, void* y, float* mean, float* rstd,
+                            int32_t* dev_status, cudaStream_t stream);
+cudaError_t launch_norm_bwd(const void* dy, const void* x, bool bf16, const void* gamma, bool param_bf16, bool rms,
+                            const float* mean, const float* rstd, const void* dres, int64_t rows, int64_t cols,
+                            void* dx, float* dgamma, float* dbeta, void* workspace, cudaStream_t stream);
+
+// Y = bf16(act(Z) + residual), Z = Xq . Wq^T / (s_x s_w) + bias; z (nullable) receives bf16(Z).
+struct LinearEpilogue {
+  const void* bias;      // [N], nullable
+  bool bias_bf16;        // else float32
+  falqon_act act;
+  const void* residual;  // bf16 [M][N], nullable
+  void* z;               // bf16 [M][N], nullable
+};
+cudaError_t launch_fp8_gemm_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                                         int64_t M, int64_t N, int64_t K, const LinearEpilogue& epi, void* y,
+                                         int32_t* dev_status, cudaStream_t stream);
+// dz = bf16(dy act'(z)) (nullable), dbias = column sums of the float32 products (nullable).
+size_t epilogue_bwd_workspace_bytes(int64_t M, int64_t N);
+cudaError_t launch_epilogue_bwd(const void* dy, const void* z, falqon_act act, int64_t M, int64_t N, void* dz,
+                                float* dbias, void* workspace, cudaStream_t stream);
+// out_s[c] = sum over p < parts of part_s[p][c], s = 0, 1; the second pair may be null.
+cudaError_t launch_column_sums(const float* part0, float* out0, const float* part1, float* out1, int parts,
+                               int64_t cols, cudaStream_t stream);
+
+// Global norm of n tensors and out = g (factor coef) (clip.cu); outs null: the norm alone.
+int64_t clip_chunk_elements();
+size_t clip_workspace_bytes();
+cudaError_t launch_clip_grads(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                              float max_norm, float factor, void* const* outs, float* norm, float* coef,
+                              int32_t* dev_status, void* workspace, cudaStream_t stream);
+
 }  // namespace falqon

@@ -31,7 +31,8 @@
  *    falqon_workspace_size(op, ...) bytes, 256-byte aligned; it may be NULL
  *    when that size is 0.  Calls that overlap on the GPU must not share a
  *    workspace.  No other aliasing between arguments is allowed except the
- *    documented in-place operands of falqon_proxy_update.
+ *    documented in-place operands of falqon_proxy_update and
+ *    falqon_clip_grads.
  *  - A workspace given to falqon_quantize or falqon_quantize_e5m2 must be
  *    initialised once, before its first use, by falqon_workspace_init (or
  *    filled with zero bytes by the caller).  Every quantize call leaves it
@@ -84,8 +85,26 @@ typedef enum falqon_op {
   FALQON_OP_SEPARATE_SAVED_FP8 = 8,  /* the same, FP8 path */
   FALQON_OP_SEPARATE_FWD_FP8 = 9,    /* workspace of the FP8 separate forward (a quantize workspace) */
   FALQON_OP_SEPARATE_BWD_BF16 = 10,  /* workspace of falqon_lora_separate_bwd, bf16 path */
-  FALQON_OP_SEPARATE_BWD_FP8 = 11    /* the same, FP8 path */
+  FALQON_OP_SEPARATE_BWD_FP8 = 11,   /* the same, FP8 path */
+  FALQON_OP_NORM_BWD = 12,           /* workspace of falqon_norm_bwd (M = rows, K = cols) */
+  FALQON_OP_LINEAR_EPILOGUE_BWD = 13, /* workspace of falqon_linear_epilogue_bwd (M, N) */
+  FALQON_OP_CLIP_GRADS = 14          /* workspace of falqon_clip_grads (no sizes) */
 } falqon_op;
+
+/* The norm of falqon_norm_fwd / falqon_norm_bwd. */
+typedef enum falqon_norm {
+  FALQON_NORM_LAYER = 0, /* mean and variance of each row */
+  FALQON_NORM_RMS = 1    /* root mean square of each row; no mean, no beta */
+} falqon_norm;
+
+/* The activation of falqon_linear_fwd_epilogue / falqon_linear_epilogue_bwd. */
+typedef enum falqon_act {
+  FALQON_ACT_NONE = 0,
+  FALQON_ACT_RELU = 1,      /* max(z, 0); derivative 0 at z = 0 */
+  FALQON_ACT_GELU_ERF = 2,  /* z Phi(z), Phi the standard normal distribution */
+  FALQON_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  FALQON_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+} falqon_act;
 
 /* Precision of the separate LoRA paths (falqon_lora_separate_fwd / _bwd). */
 typedef enum falqon_separate_precision {
@@ -530,6 +549,120 @@ FALQON_API const char* falqon_status_string(falqon_status status);
 
 /* Library version string. */
 FALQON_API const char* falqon_version(void);
+
+/*
+ * falqon_norm_fwd / falqon_norm_bwd - layer norm or RMS norm of each row: the
+ * operator in front of a quantized activation.
+ *
+ * The pages describe the linear layer alone; in the transformer blocks they
+ * fine-tune, the activation that falqon_quantize reads is a norm's output.
+ *   layer  mu = mean(x), rstd = 1 / sqrt(mean((x - mu)^2) + eps), xh = (x - mu) rstd
+ *   rms    rstd = 1 / sqrt(mean(x^2) + eps), xh = x rstd
+ *   y = xh gamma + beta
+ *   g = dy gamma, c1 = mean(g) (0 for rms), c2 = mean(g xh)
+ *   dx = rstd (g - c1 - xh c2) + dres
+ *   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
+ * Everything is computed in float32 and rounded once per output element; the
+ * sums over rows are joined in a fixed order (the same call gives the same
+ * bits).
+ *
+ *  x, y, dy, dres, dx [rows, cols] in `dtype` (bfloat16 or float32).  dres,
+ *  nullable, is a gradient that joins dx: that of the residual branch around
+ *  the norm.
+ *  gamma, beta [cols] in `param_dtype`; each nullable (1 and 0).  beta must be
+ *  NULL for FALQON_NORM_RMS.
+ *  mean, rstd [rows] float32: written by the forward (each nullable; mean must
+ *  be NULL for RMS), read by the backward (rstd always, mean for LAYER, NULL
+ *  for RMS).
+ *  dx, dgamma [cols], dbeta [cols] (float32 sums): each nullable, at least one
+ *  wanted; dbeta must be NULL for RMS, dres needs dx.
+ *  eps >= 0 and finite.
+ *  workspace (dgamma or dbeta wanted): falqon_workspace_size(
+ *  FALQON_OP_NORM_BWD, rows, 0, cols, 0) bytes.
+ *  Requirements: rows, cols >= 1 and below 2^31 - 256; cols need not be a
+ *  multiple of anything (multiples of 8, 4 in float32, move in 16-byte
+ *  vectors).
+ *  Device status (forward): NONFINITE when a row's statistics are not finite
+ *  (an infinity or NaN in it, or squares past float32) or its rstd is 0 or
+ *  infinite (eps = 0 on a constant row).
+ */
+FALQON_API falqon_status falqon_norm_fwd(const void* x, falqon_dtype dtype, const void* gamma, const void* beta,
+                                         falqon_dtype param_dtype, falqon_norm kind, int64_t rows, int64_t cols,
+                                         float eps, void* y, float* mean, float* rstd, int32_t* dev_status,
+                                         void* stream);
+FALQON_API falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_dtype dtype, const void* gamma,
+                                         falqon_dtype param_dtype, falqon_norm kind, const float* mean,
+                                         const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
+                                         float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
+/*
+ * falqon_linear_fwd_epilogue - falqon_linear_fwd with a bias, an activation
+ * and a residual in the GEMM's epilogue.
+ *
+ *   Z = Xq . Wq^T / (s_X s_W) + bias,   Y = bf16( act(Z) + residual )
+ * in float32 from the accumulators on, rounded once; z, when wanted, receives
+ * bf16(Z) for the backward.
+ *
+ *  xq, s_x, wq, s_w as falqon_linear_fwd.  bias [N] in bias_dtype, nullable.
+ *  residual [M, N] bfloat16, nullable; it may not be y or z.
+ *  z [M, N] bfloat16, nullable; y [M, N] bfloat16.
+ *  Requirements: as falqon_linear_fwd.
+ */
+FALQON_API falqon_status falqon_linear_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq,
+                                                    const float* s_w, const void* bias, falqon_dtype bias_dtype,
+                                                    falqon_act act, const void* residual, int64_t M, int64_t N,
+                                                    int64_t K, void* z, void* y, int32_t* dev_status, void* stream);
+
+/*
+ * falqon_linear_epilogue_bwd - backward of that epilogue.
+ *
+ *   dZ = bf16( dY act'(Z) ),   dbias[n] = sum over m of dY[m,n] act'(Z[m,n])
+ * dbias sums the float32 products, before dZ's rounding, in a fixed order.
+ * dZ is what falqon_quantize and falqon_linear_bwd then take as the layer's
+ * output gradient; the residual's gradient is dY itself.
+ *
+ *  dy [M, N] bfloat16; z [M, N] bfloat16 as the forward kept it (may be NULL
+ *  for FALQON_ACT_NONE, whose dZ is dY).
+ *  dz [M, N] bfloat16, dbias [N] float32: each nullable, at least one wanted.
+ *  workspace (dbias wanted): falqon_workspace_size(
+ *  FALQON_OP_LINEAR_EPILOGUE_BWD, M, N, 0, 0) bytes.
+ *  Requirements: M >= 1; N a multiple of 16; both below 2^31 - 256.
+ */
+FALQON_API falqon_status falqon_linear_epilogue_bwd(const void* dy, const void* z, falqon_act act, int64_t M,
+                                                    int64_t N, void* dz, float* dbias, void* workspace,
+                                                    size_t workspace_bytes, void* stream);
+
+/*
+ * falqon_clip_grads - the global norm of many gradients, and the gradients
+ * scaled by it: the step between falqon_linear_bwd and falqon_proxy_update.
+ *
+ *   norm = sqrt( sum of g^2 over every element of every tensor )
+ *   coef = max_norm / norm where norm > max_norm, else 1
+ *   out  = g * fl32(factor * coef), rounded once to g's type
+ * With factor = -lr the outputs are the increments dB_inc of a plain SGD step.
+ * The squares are summed in float64 above single vectors and joined in a
+ * fixed order.  A gradient holding an infinity or NaN makes the whole step
+ * void: norm reports it, coef is 0, every output is +0 and the status word
+ * gets NONFINITE.
+ *
+ *  n >= 1 tensors.  grads, dtypes, numel: HOST arrays of n entries: device
+ *  pointer (16-byte aligned), element type, element count (0 allowed; the
+ *  pointers are then not used).  outs: HOST array of n device pointers, types
+ *  and counts as the gradients'; outs[i] may be grads[i] (in place) but may
+ *  overlap no other gradient or output (FALQON_ERR_INVALID_ARG).  outs NULL:
+ *  the norm alone.  The host arrays are read before the call returns.
+ *  max_norm > 0 (INFINITY: no clipping); factor finite.
+ *  norm 1 float (written; infinity above float32), coef 1 float (nullable).
+ *  workspace: falqon_workspace_size(FALQON_OP_CLIP_GRADS, 0, 0, 0, 0) bytes.
+ *  Requirements: numel[i] <= 2^42; fewer than 2^31 chunks of 4096 elements.
+ *  Launches: two for up to 512 tensors that hold elements, two more for each
+ *  further 512.
+ */
+FALQON_API falqon_status falqon_clip_grads(int n, const void* const* grads, const falqon_dtype* dtypes,
+                                           const int64_t* numel, float max_norm, float factor, void* const* outs,
+                                           float* norm, float* coef, int32_t* dev_status, void* workspace,
+                                           size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
