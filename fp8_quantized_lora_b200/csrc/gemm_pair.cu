@@ -37,8 +37,18 @@
 //
 // kEpi: the forward with a bias, an activation, a residual and a kept
 // pre-activation in its epilogue (falqon_linear_fwd_epilogue); the plain
-// products are compiled without that code.
+// products are compiled without that code.  Up to three matrices of M x N bf16
+// then pass through the epilogue beside the accumulator, and a lane, which
+// holds one row of it, would reach each of them 16 bytes at a time in 32 rows
+// at once.  So each of eight epilogue warps (two per TMEM quarter, every other
+// slab each) moves its 32-row x 32-column slabs by TMA through shared memory
+// of its own, 64-byte swizzled (conflict-free 16-byte accesses along a row per
+// lane): the residual is fetched two slabs ahead and the bias one (a lane
+// holds one column's, shared memory spreads it), Z and Y leave as bulk stores.
+// No warp waits for another.  The 64 KB of slabs cost the ring one of
+// its six stages.
 #include <algorithm>
+#include <type_traits>
 
 #include "act.cuh"
 #include "elem.cuh"
@@ -62,57 +72,54 @@ struct PairArgs {
   LinearEpilogue epi;      // kEpi only; z and residual are [M][ldo] as out
 };
 
-// Eight consecutive elements of the bias as float32.
-__device__ __forceinline__ void load_bias8(const LinearEpilogue& e, int64_t col, float (&b)[8]) {
-  if (e.bias_bf16) {
-    unpack16<true>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(e.bias) + col)), b);
-  } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + col);
-    const float4 lo = __ldg(p), hi = __ldg(p + 1);
-    b[0] = lo.x; b[1] = lo.y; b[2] = lo.z; b[3] = lo.w;
-    b[4] = hi.x; b[5] = hi.y; b[6] = hi.z; b[7] = hi.w;
-  }
-}
+// One lane's row of a slab: 32 accumulators scaled, bias, Z, activation,
+// residual, Y.  `bias`: the slab's 32 biases in shared memory; `res`, `zs`,
+// `ys`: the slab's images there (null: not wanted).
+constexpr int kSlab = 32;                        // rows and columns
+constexpr int kSlabBytes = kSlab * kSlab * 2;
 
 template <int kAct>
-__device__ __forceinline__ void act8(float (&v)[8]) {
+__device__ __forceinline__ void epilogue_slab(const uint32_t (&r)[32], float alpha, int lane, const float* bias,
+                                              const uint8_t* res, uint8_t* zs, uint8_t* ys) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = act_value<kAct>(v[j]);
+  for (int j = 0; j < 4; ++j) {
+    const int at = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);  // 16-byte unit j of the 64-byte swizzled row
+    const float4 b0 = reinterpret_cast<const float4*>(bias)[2 * j], b1 = reinterpret_cast<const float4*>(bias)[2 * j + 1];
+    float v[8], b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+    for (int h = 0; h < 8; ++h) v[h] = fmaf(__uint_as_float(r[8 * j + h]), alpha, b[h]);
+    if (zs) *reinterpret_cast<uint4*>(zs + at) = pack16<true>(v);
+#pragma unroll
+    for (int h = 0; h < 8; ++h) v[h] = act_value<kAct>(v[h]);
+    if (res) {
+      unpack16<true>(*reinterpret_cast<const uint4*>(res + at), b);
+#pragma unroll
+      for (int h = 0; h < 8; ++h) v[h] += b[h];
+    }
+    *reinterpret_cast<uint4*>(ys + at) = pack16<true>(v);
+  }
 }
 
-__device__ __forceinline__ void act8(falqon_act act, float (&v)[8]) {
+__device__ __forceinline__ void epilogue_slab(falqon_act act, const uint32_t (&r)[32], float alpha, int lane,
+                                              const float* bias, const uint8_t* res, uint8_t* zs, uint8_t* ys) {
   switch (act) {
-    case FALQON_ACT_RELU: act8<FALQON_ACT_RELU>(v); break;
-    case FALQON_ACT_GELU_ERF: act8<FALQON_ACT_GELU_ERF>(v); break;
-    case FALQON_ACT_GELU_TANH: act8<FALQON_ACT_GELU_TANH>(v); break;
-    case FALQON_ACT_SILU: act8<FALQON_ACT_SILU>(v); break;
-    default: break;
+    case FALQON_ACT_NONE: epilogue_slab<FALQON_ACT_NONE>(r, alpha, lane, bias, res, zs, ys); break;
+    case FALQON_ACT_RELU: epilogue_slab<FALQON_ACT_RELU>(r, alpha, lane, bias, res, zs, ys); break;
+    case FALQON_ACT_GELU_ERF: epilogue_slab<FALQON_ACT_GELU_ERF>(r, alpha, lane, bias, res, zs, ys); break;
+    case FALQON_ACT_GELU_TANH: epilogue_slab<FALQON_ACT_GELU_TANH>(r, alpha, lane, bias, res, zs, ys); break;
+    case FALQON_ACT_SILU: epilogue_slab<FALQON_ACT_SILU>(r, alpha, lane, bias, res, zs, ys); break;
   }
 }
 
-// Eight scaled accumulators through the epilogue: bias, z, activation,
-// residual, one rounding to bf16.  `at`: element offset of the first one.
-__device__ __forceinline__ void store_epilogue8(const LinearEpilogue& e, void* out, int64_t at, int64_t col,
-                                                float (&v)[8]) {
-  if (e.bias) {
-    float b[8];
-    load_bias8(e, col, b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += b[j];
-  }
-  if (e.z) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.z) + at) = pack16<true>(v);
-  act8(e.act, v);
-  if (e.residual) {
-    float r[8];
-    unpack16<true>(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.residual) + at), r);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += r[j];
-  }
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at) = pack16<true>(v);
-}
+// The tensor maps of the epilogue's matrices (boxes of one slab).
+struct EpiMaps {
+  CUtensorMap y, z, res;
+};
+struct NoMaps {};
 
-template <bool kBMn, uint32_t kAFmt, int kStages>
+template <bool kBMn, uint32_t kAFmt, int kStages, bool kEpi = false>
 struct PairCfg {
+  static constexpr bool Epi = kEpi;
   static constexpr bool BMn = kBMn;
   static constexpr int Stages = kStages;
   static constexpr int TileM = 2 * kBM;         // 256: 128 rows per CTA
@@ -124,24 +131,31 @@ struct PairCfg {
   static constexpr int StageBytes = ABytes + BBytes;
   static constexpr int Acc = 2;
   static constexpr uint32_t TmemCols = 512;     // two accumulators of 256 columns
-  static constexpr int EpiWarps = 4;
-  static constexpr int WaiterWarp = 6;
+  static constexpr int EpiWarps = kEpi ? 8 : 4;
+  static constexpr int WaiterWarp = 2 + EpiWarps;
   static constexpr int Threads = 32 * (WaiterWarp + 1);
   static constexpr int BarBytes = 8 * (2 * kStages + 2 * Acc + 1) + 16;
-  static constexpr int SmemBytes = kStages * StageBytes + BarBytes + 1024;
+  // kEpi, per epilogue warp: two residual slabs, a Z slab and a Y slab (two Y
+  // slabs in turn without Z), the slab's biases, and two barriers of the
+  // residual's loads
+  static constexpr int WarpSlabs = 4;
+  static constexpr int EpiBytes = kEpi ? EpiWarps * (WarpSlabs * kSlabBytes + kSlab * 4 + 16) : 0;
+  static constexpr int SmemBytes = kStages * StageBytes + EpiBytes + BarBytes + 1024;
   static constexpr uint32_t IDesc = idesc_f32acc(kAFmt, 0u, 0u, kBMn ? 1u : 0u, 256, TileN);
   static constexpr uint32_t IDescHalf = idesc_f32acc(kAFmt, 0u, 0u, kBMn ? 1u : 0u, 256, TileN / 2);
   static_assert(SmemBytes <= 232448, "shared memory per CTA");
 };
 
-template <class C, bool kEpi>
+template <class C>
 __global__ void __launch_bounds__(C::Threads, 1)
     tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmBh, const PairArgs g) {
+                        const __grid_constant__ CUtensorMap tmBh, const PairArgs g,
+                        const __grid_constant__ std::conditional_t<C::Epi, EpiMaps, NoMaps> em) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::Stages * C::StageBytes);
+  uint8_t* slabs = smem + C::Stages * C::StageBytes;  // [EpiWarps][WarpSlabs] (kEpi)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::Stages * C::StageBytes + C::EpiBytes);
   uint64_t* full = bars;                      // [Stages] both CTAs' tiles landed (even CTA's copy is used)
   uint64_t* empty = bars + C::Stages;         // [Stages] the MMAs are done with this CTA's slot
   uint64_t* acc_full = bars + 2 * C::Stages;  // [Acc] accumulator ready (both CTAs)
@@ -178,6 +192,13 @@ __global__ void __launch_bounds__(C::Threads, 1)
       mbar_init(&acc_empty[b], 2 * C::EpiWarps);
     }
     mbar_init(drain, 1);
+    if constexpr (C::Epi) {
+      uint64_t* landed = reinterpret_cast<uint64_t*>(slabs + C::EpiWarps * (C::WarpSlabs * kSlabBytes + kSlab * 4));
+      for (int i = 0; i < 2 * C::EpiWarps; ++i) mbar_init(&landed[i], 1);
+      tma_prefetch_desc(&em.y);
+      if (g.epi.z) tma_prefetch_desc(&em.z);
+      if (g.epi.residual) tma_prefetch_desc(&em.res);
+    }
     *abort_flag = 0;
     fence_barrier_init();  // visible to the other CTA's copies and arrivals
     tma_prefetch_desc(&tmA);
@@ -314,49 +335,164 @@ __global__ void __launch_bounds__(C::Threads, 1)
       if (g.scale_b) den *= static_cast<double>(*g.scale_b);
       alpha = static_cast<float>(1.0 / den);
     }
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int w = pair; w < total; w += npairs) {
-      int mt, nt, nh;
-      item(w, mt, nt, nh);
-      if (!warp_wait(&acc_full[acc], acc_phase, abort_flag)) { if (lane == 0) fail(); break; }
-      tc_fence_after();
-      const int64_t row = static_cast<int64_t>(mt) * C::TileM + rank * kBM + q * 32 + lane;
-      const int64_t col_base = static_cast<int64_t>(nt) * C::TileN + (nh > 0 ? C::TileN / 2 : 0);
-      const int chunks = (nh >= 0 ? C::TileN / 2 : C::TileN) / 32;
+    if constexpr (C::Epi) {
+      const int half = (warp - 2) >> 2;  // this warp takes every other slab of its quarter
+      uint8_t* own = slabs + (warp - 2) * C::WarpSlabs * kSlabBytes;
+      uint8_t* out = own + 2 * kSlabBytes;
+      float* biases = reinterpret_cast<float*>(slabs + C::EpiWarps * C::WarpSlabs * kSlabBytes) + (warp - 2) * kSlab;
+      uint64_t* landed =
+          reinterpret_cast<uint64_t*>(slabs + C::EpiWarps * (C::WarpSlabs * kSlabBytes + kSlab * 4)) + 2 * (warp - 2);
+      const bool has_res = g.epi.residual != nullptr, has_z = g.epi.z != nullptr;
+      // slab i of this warp in work item w: its place, and whether any of it exists
+      auto place = [&](int w, int i, int& row0, int& col) {
+        int mt, nt, nh;
+        item(w, mt, nt, nh);
+        row0 = mt * C::TileM + static_cast<int>(rank) * kBM + q * 32;
+        col = nt * C::TileN + (nh > 0 ? C::TileN / 2 : 0) + (2 * i + half) * kSlab;
+        return row0 < g.M && col < g.N;
+      };
+      auto slab_count = [&](int w) { return (w >= g.n_full ? C::TileN / 2 : C::TileN) / kSlab / 2; };
+      // the residual's slabs are fetched in the order of use into two buffers in turn
+      int pw = pair, pi = 0;
+      uint32_t fetched = 0, used = 0;
+      auto fetch = [&]() {
+        while (pw < total) {
+          int row0, col;
+          const bool there = place(pw, pi, row0, col);
+          if (++pi == slab_count(pw)) {
+            pi = 0;
+            pw += npairs;
+          }
+          if (!there) continue;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&landed[fetched & 1u], kSlabBytes);
+            tma_load_2d(own + (fetched & 1u) * kSlabBytes, &em.res, &landed[fetched & 1u], col, row0);
+          }
+          ++fetched;
+          return;
+        }
+      };
+      // the bias of this lane's column of the next slab
+      int bw = pair, bi = 0;
+      auto next_bias = [&]() {
+        while (bw < total) {
+          int row0, col;
+          const bool there = place(bw, bi, row0, col);
+          if (++bi == slab_count(bw)) {
+            bi = 0;
+            bw += npairs;
+          }
+          if (there) return g.epi.bias && col + lane < g.N ? load_param(g.epi.bias, g.epi.bias_bf16, col + lane, 0.0f) : 0.0f;
+        }
+        return 0.0f;
+      };
+      if (has_res) {
+        fetch();
+        fetch();
+      }
+      float bias = next_bias();
+      int acc = 0;
+      uint32_t acc_phase = 0, turn = 0;
+      bool ok = true;
+      for (int w = pair; w < total && ok; w += npairs) {
+        if (!warp_wait(&acc_full[acc], acc_phase, abort_flag)) { if (lane == 0) fail(); break; }
+        tc_fence_after();
+        const int n = slab_count(w);
 #pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        uint32_t r[32];
-        tmem_ld_32cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * C::TileN + c * 32),
-                       r);
-        tmem_ld_wait();
-        if (row < g.M) {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(g.out) + row * g.ldo;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t col = col_base + c * 32 + 8 * j;
-            if (kEpi && col < g.N) {
-              float v[8];
-#pragma unroll
-              for (int h = 0; h < 8; ++h) v[h] = __uint_as_float(r[8 * j + h]) * alpha;
-              store_epilogue8(g.epi, g.out, row * g.ldo + col, col, v);
-            } else if (!kEpi && col < g.N) {  // N % 8 == 0: eight columns in or out together
-              uint32_t pk[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * h]) * alpha,
-                                                               __uint_as_float(r[8 * j + 2 * h + 1]) * alpha);
-                memcpy(&pk[h], &b, 4);
+        for (int i = 0; i < n; ++i) {
+          int row0, col;
+          const bool there = place(w, i, row0, col);
+          uint32_t r[32];
+          if (there) {
+            tmem_ld_32cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                               static_cast<uint32_t>(acc * C::TileN + (2 * i + half) * kSlab),
+                           r);
+            tmem_ld_wait();
+          }
+          if (i == n - 1) {  // this warp's part of the accumulator is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_lead + 8u * static_cast<uint32_t>(acc));
+          }
+          if (!there) continue;
+          const uint8_t* res = nullptr;
+          if (has_res) {
+            if (!warp_wait(&landed[used & 1u], (used >> 1) & 1u, abort_flag)) {
+              if (lane == 0) fail();
+              ok = false;
+              break;
+            }
+            res = own + (used & 1u) * kSlabBytes;
+          }
+          biases[lane] = bias;  // every lane is past the last slab's
+          bias = next_bias();
+          // the stores that read these buffers last are done reading them
+          if (lane == 0) {
+            if (has_z) bulk_wait_read<0>();
+            else bulk_wait_read<1>();
+          }
+          __syncwarp();
+          uint8_t* ys = out + (has_z ? kSlabBytes : (turn & 1u) * kSlabBytes);
+          epilogue_slab(g.epi.act, r, alpha, lane, biases, res, has_z ? out : nullptr, ys);
+          fence_proxy_async_smem();  // the slabs are visible to the bulk stores
+          __syncwarp();
+          if (lane == 0) {
+            if (has_z) tma_store_2d(&em.z, out, col, row0);
+            tma_store_2d(&em.y, ys, col, row0);
+            bulk_commit();
+          }
+          ++turn;
+          if (has_res) {  // every lane has read its row of the slab
+            ++used;
+            fetch();
+          }
+        }
+        if (++acc == C::Acc) { acc = 0; acc_phase ^= 1; }
+      }
+      // after an abort: what was fetched and not used has landed before the memory goes
+      for (; used < fetched; ++used) mbar_wait_budget(&landed[used & 1u], (used >> 1) & 1u);
+      if (lane == 0) bulk_wait_read<0>();  // the stores no longer read this CTA's memory
+      __syncwarp();
+    } else {
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      for (int w = pair; w < total; w += npairs) {
+        int mt, nt, nh;
+        item(w, mt, nt, nh);
+        if (!warp_wait(&acc_full[acc], acc_phase, abort_flag)) { if (lane == 0) fail(); break; }
+        tc_fence_after();
+        const int64_t row = static_cast<int64_t>(mt) * C::TileM + rank * kBM + q * 32 + lane;
+        const int64_t col_base = static_cast<int64_t>(nt) * C::TileN + (nh > 0 ? C::TileN / 2 : 0);
+        const int chunks = (nh >= 0 ? C::TileN / 2 : C::TileN) / 32;
+  #pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+          uint32_t r[32];
+          tmem_ld_32cols(tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * C::TileN + c * 32),
+                         r);
+          tmem_ld_wait();
+          if (row < g.M) {
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(g.out) + row * g.ldo;
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int64_t col = col_base + c * 32 + 8 * j;
+              if (col < g.N) {  // N % 8 == 0: eight columns in or out together
+                uint32_t pk[4];
+  #pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(r[8 * j + 2 * h]) * alpha,
+                                                                 __uint_as_float(r[8 * j + 2 * h + 1]) * alpha);
+                  memcpy(&pk[h], &b, 4);
+                }
+                *reinterpret_cast<uint4*>(dst + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
-              *reinterpret_cast<uint4*>(dst + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(empty_lead + 8u * static_cast<uint32_t>(acc));
+        if (++acc == C::Acc) { acc = 0; acc_phase ^= 1; }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(empty_lead + 8u * static_cast<uint32_t>(acc));
-      if (++acc == C::Acc) { acc = 0; acc_phase ^= 1; }
     }
   }
 
@@ -373,10 +509,11 @@ __global__ void __launch_bounds__(C::Threads, 1)
 using PairFwdCfg = PairCfg<false, 0u, 6>;
 using PairDxCfg = PairCfg<true, 0u, 6>;
 using PairDxE5Cfg = PairCfg<true, 1u, 6>;  // dYq in E5M2
+using PairEpiCfg = PairCfg<false, 0u, 5, true>;
 
 // Pairs the device can keep resident at once (cached per device): the grid
 // never exceeds it, so the persistent pairs all run in one wave.
-template <class C, bool kEpi>
+template <class C>
 int resident_pairs(const DeviceInfo* di) {
   static int cached[32] = {0};
   const int dev = di->device;
@@ -393,7 +530,7 @@ int resident_pairs(const DeviceInfo* di) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_pair_kernel<C, kEpi>, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_pair_kernel<C>, &cfg) != cudaSuccess || n <= 0) {
     cudaGetLastError();
     n = di->sm_count / 2;
   }
@@ -402,7 +539,7 @@ int resident_pairs(const DeviceInfo* di) {
   return n;
 }
 
-template <class C, bool kEpi = false>
+template <class C>
 cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const float* sb, int64_t M,
                       int64_t Ncols, int64_t Kc, void* out, int32_t* dev_status, cudaStream_t stream,
                       const LinearEpilogue& epi = {}) {
@@ -411,7 +548,7 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
   static int configured_mask = 0;  // one bit per device ordinal < 31
   const int bit = di->device < 31 ? (1 << di->device) : 0;
   if (!bit || !(__atomic_load_n(&configured_mask, __ATOMIC_ACQUIRE) & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(tc_gemm_pair_kernel<C, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(tc_gemm_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SmemBytes);
     if (e != cudaSuccess) return e;
     if (bit) __atomic_fetch_or(&configured_mask, bit, __ATOMIC_ACQ_REL);
@@ -428,6 +565,14 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
     if (!make_tmap_2d(&tB, U8, 1, b, Kc, Ncols, C::BK, C::TileN / 2, true)) return cudaErrorInvalidValue;
     if (!make_tmap_2d(&tBh, U8, 1, b, Kc, Ncols, C::BK, C::TileN / 4, true)) return cudaErrorInvalidValue;
   }
+  std::conditional_t<C::Epi, EpiMaps, NoMaps> em{};
+  if constexpr (C::Epi) {
+    const auto B16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    if (!make_tmap_2d_sw64(&em.y, B16, 2, out, Ncols, M, kSlab, kSlab)) return cudaErrorInvalidValue;
+    if (epi.z && !make_tmap_2d_sw64(&em.z, B16, 2, epi.z, Ncols, M, kSlab, kSlab)) return cudaErrorInvalidValue;
+    if (epi.residual && !make_tmap_2d_sw64(&em.res, B16, 2, epi.residual, Ncols, M, kSlab, kSlab))
+      return cudaErrorInvalidValue;
+  }
   PairArgs g{};
   g.m_tiles = ceil_div(M, C::TileM);
   g.n_tiles = ceil_div(Ncols, C::TileN);
@@ -442,7 +587,7 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
   g.epi = epi;
   const int tiles = g.m_tiles * g.n_tiles;
   if (tiles == 0) return cudaSuccess;
-  const int slots = resident_pairs<C, kEpi>(di);
+  const int slots = resident_pairs<C>(di);
   const int pairs = tiles < slots ? tiles : slots;
   // a partial last wave of at most half the pairs runs as 256 x 128 halves
   const int tail = tiles % pairs;
@@ -452,8 +597,8 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
     g.n_full = tiles - tail;
     g.n_half = 2 * tail;
   }
-  return launch_pdl(tc_gemm_pair_kernel<C, kEpi>, dim3(static_cast<unsigned>(2 * pairs)), dim3(C::Threads), C::SmemBytes,
-                    stream, 2u, tA, tB, tBh, g);
+  return launch_pdl(tc_gemm_pair_kernel<C>, dim3(static_cast<unsigned>(2 * pairs)), dim3(C::Threads), C::SmemBytes,
+                    stream, 2u, tA, tB, tBh, g, em);
 }
 
 }  // namespace
@@ -467,7 +612,7 @@ cudaError_t launch_fp8_gemm_fwd_pair(const uint8_t* xq, const float* s_x, const 
 cudaError_t launch_fp8_gemm_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
                                          int64_t M, int64_t N, int64_t K, const LinearEpilogue& epi, void* y,
                                          int32_t* dev_status, cudaStream_t stream) {
-  return pair_gemm<PairFwdCfg, true>(xq, s_x, wq, s_w, M, N, K, y, dev_status, stream, epi);
+  return pair_gemm<PairEpiCfg>(xq, s_x, wq, s_w, M, N, K, y, dev_status, stream, epi);
 }
 
 cudaError_t launch_fp8_gemm_dx_pair(const uint8_t* dyq, const float* s_dy, const uint8_t* wq, const float* s_w,
