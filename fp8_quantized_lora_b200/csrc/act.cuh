@@ -36,23 +36,58 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// Two float32 operations in one instruction (each rounded as its scalar form).
+__device__ __forceinline__ uint64_t f2_bits(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 f2_of(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluTwoU = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluCubic = 0.044715f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
+// P: the coefficients of t^0 .. t^7.
+__host__ __device__ constexpr float tail_coef(int k) {
+  return k == 0   ? 0.248216525f
+         : k == 1 ? 0.248935506f
+         : k == 2 ? 0.21693407f
+         : k == 3 ? 0.216996044f
+         : k == 4 ? -0.0222996026f
+         : k == 5 ? 0.298873633f
+         : k == 6 ? -0.279156834f
+                  : 0.0715008602f;
+}
+
 // exp(-z^2 / 2) and erfc(|z| / sqrt 2).
 __device__ __forceinline__ void normal_tail(float z, float& e, float& h) {
   e = exp2_fast(z * z * (-0.5f * kLog2E));
   const float t = rcp_fast(fmaf(0.311126984f, fabsf(z), 1.0f));
-  float p = 0.0715008602f;
-  p = fmaf(p, t, -0.279156834f);
-  p = fmaf(p, t, 0.298873633f);
-  p = fmaf(p, t, -0.0222996026f);
-  p = fmaf(p, t, 0.216996044f);
-  p = fmaf(p, t, 0.21693407f);
-  p = fmaf(p, t, 0.248935506f);
-  p = fmaf(p, t, 0.248216525f);
+  float p = tail_coef(7);
+#pragma unroll
+  for (int k = 6; k >= 0; --k) p = fmaf(p, t, tail_coef(k));
   h = p * t * e;
 }
 
@@ -76,6 +111,32 @@ __device__ __forceinline__ float act_value(float z) {
   if constexpr (kAct == FALQON_ACT_GELU_TANH) return z * rcp_fast(1.0f + exp2_fast(gelu_exponent(z, z * z)));
   if constexpr (kAct == FALQON_ACT_SILU) return z * rcp_fast(1.0f + exp2_fast(-kLog2E * z));
   return z;
+}
+
+// Two values at once: the same operations, two to an instruction where there is
+// one for two.
+template <int kAct>
+__device__ __forceinline__ float2 act_value2(float2 z) {
+  if constexpr (kAct == FALQON_ACT_GELU_TANH || kAct == FALQON_ACT_SILU) {
+    float2 n;
+    if constexpr (kAct == FALQON_ACT_SILU)
+      n = mul2(z, both(-kLog2E));
+    else
+      n = mul2(z, fma2(mul2(z, z), both(-kGeluTwoU * kLog2E * kGeluCubic), both(-kGeluTwoU * kLog2E)));
+    const float2 d = add2(make_float2(exp2_fast(n.x), exp2_fast(n.y)), both(1.0f));
+    return mul2(z, make_float2(rcp_fast(d.x), rcp_fast(d.y)));
+  }
+  if constexpr (kAct == FALQON_ACT_GELU_ERF) {
+    const float2 q = mul2(mul2(z, z), both(-0.5f * kLog2E));
+    const float2 d = fma2(both(0.311126984f), make_float2(fabsf(z.x), fabsf(z.y)), both(1.0f));
+    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    float2 p = both(tail_coef(7));
+#pragma unroll
+    for (int k = 6; k >= 0; --k) p = fma2(p, t, both(tail_coef(k)));
+    const float2 h = mul2(mul2(p, t), make_float2(exp2_fast(q.x), exp2_fast(q.y)));
+    return mul2(z, make_float2(normal_cdf(z.x, h.x), normal_cdf(z.y, h.y)));
+  }
+  return make_float2(act_value<kAct>(z.x), act_value<kAct>(z.y));
 }
 
 // p + zu p (1 - p) for p = 1 / (1 + 2^n): with e = 2^-|n| <= 1 and

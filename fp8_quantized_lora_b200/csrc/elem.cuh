@@ -28,6 +28,14 @@ __device__ __forceinline__ void unpack16(const uint4& q, float (&v)[kVec<kBF16>]
   }
 }
 
+// Two values rounded to bf16, the first in the low half.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  uint32_t w;
+  memcpy(&w, &b, 4);
+  return w;
+}
+
 // Rounded once, to nearest even (bf16), or kept (float32).
 template <bool kBF16>
 __device__ __forceinline__ uint4 pack16(const float (&v)[kVec<kBF16>]) {
@@ -35,8 +43,7 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[kVec<kBF16>]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if constexpr (kBF16) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-      memcpy(&w[j], &b, 4);
+      w[j] = pack2(v[2 * j], v[2 * j + 1]);
     } else {
       w[j] = __float_as_uint(v[j]);
     }

@@ -48,7 +48,6 @@
 // No warp waits for another.  The 64 KB of slabs cost the ring one of
 // its six stages.
 #include <algorithm>
-#include <type_traits>
 
 #include "act.cuh"
 #include "elem.cuh"
@@ -70,52 +69,57 @@ struct PairArgs {
   const float* scale_b;
   int32_t* dev_status;
   LinearEpilogue epi;      // kEpi only; z and residual are [M][ldo] as out
+  bool wide;               // kEpi: out, z and residual are 32-byte aligned
 };
 
 // One lane's row of a slab: 32 accumulators scaled, bias, Z, activation,
-// residual, Y.  `bias`: the slab's 32 biases in shared memory; `res`, `zs`,
-// `ys`: the slab's images there (null: not wanted).
-constexpr int kSlab = 32;                        // rows and columns
-constexpr int kSlabBytes = kSlab * kSlab * 2;
+// residual, Y.  `bias`: the slab's 32 biases in shared memory; `res`: the
+// residual's 32 values; `z`, `y`: the row in memory (null: not wanted), of
+// which the first `cols` columns (16 or 32) exist.
+constexpr int kSlab = 32;  // rows and columns
 
 template <int kAct>
-__device__ __forceinline__ void epilogue_slab(const uint32_t (&r)[32], float alpha, int lane, const float* bias,
-                                              const uint8_t* res, uint8_t* zs, uint8_t* ys) {
+__device__ __forceinline__ void epilogue_slab(const uint32_t (&r)[32], float alpha, const float* bias, bool has_res,
+                                              const uint32_t (&res)[16], __nv_bfloat16* z, __nv_bfloat16* y, int cols,
+                                              bool wide) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);  // 16-byte unit j of the 64-byte swizzled row
-    const float4 b0 = reinterpret_cast<const float4*>(bias)[2 * j], b1 = reinterpret_cast<const float4*>(bias)[2 * j + 1];
-    float v[8], b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+  for (int j = 0; j < 2; ++j) {
+    float2 v[8];
+    uint32_t pk[8];
 #pragma unroll
-    for (int h = 0; h < 8; ++h) v[h] = fmaf(__uint_as_float(r[8 * j + h]), alpha, b[h]);
-    if (zs) *reinterpret_cast<uint4*>(zs + at) = pack16<true>(v);
-#pragma unroll
-    for (int h = 0; h < 8; ++h) v[h] = act_value<kAct>(v[h]);
-    if (res) {
-      unpack16<true>(*reinterpret_cast<const uint4*>(res + at), b);
-#pragma unroll
-      for (int h = 0; h < 8; ++h) v[h] += b[h];
+    for (int h = 0; h < 8; ++h) {
+      const float2 a = make_float2(__uint_as_float(r[16 * j + 2 * h]), __uint_as_float(r[16 * j + 2 * h + 1]));
+      v[h] = fma2(a, both(alpha), reinterpret_cast<const float2*>(bias)[8 * j + h]);
     }
-    *reinterpret_cast<uint4*>(ys + at) = pack16<true>(v);
+    if (z) {
+#pragma unroll
+      for (int h = 0; h < 8; ++h) pk[h] = pack2(v[h].x, v[h].y);
+      if (16 * j < cols) store_global_32B(z + 16 * j, wide, pk);
+    }
+#pragma unroll
+    for (int h = 0; h < 8; ++h) v[h] = act_value2<kAct>(v[h]);
+    if (has_res) {
+#pragma unroll
+      for (int h = 0; h < 8; ++h)
+        v[h] = add2(v[h], make_float2(__uint_as_float(res[8 * j + h] << 16), __uint_as_float(res[8 * j + h] & 0xFFFF0000u)));
+    }
+#pragma unroll
+    for (int h = 0; h < 8; ++h) pk[h] = pack2(v[h].x, v[h].y);
+    if (y && 16 * j < cols) store_global_32B(y + 16 * j, wide, pk);
   }
 }
 
-__device__ __forceinline__ void epilogue_slab(falqon_act act, const uint32_t (&r)[32], float alpha, int lane,
-                                              const float* bias, const uint8_t* res, uint8_t* zs, uint8_t* ys) {
+__device__ __forceinline__ void epilogue_slab(falqon_act act, const uint32_t (&r)[32], float alpha, const float* bias,
+                                              bool has_res, const uint32_t (&res)[16], __nv_bfloat16* z,
+                                              __nv_bfloat16* y, int cols, bool wide) {
   switch (act) {
-    case FALQON_ACT_NONE: epilogue_slab<FALQON_ACT_NONE>(r, alpha, lane, bias, res, zs, ys); break;
-    case FALQON_ACT_RELU: epilogue_slab<FALQON_ACT_RELU>(r, alpha, lane, bias, res, zs, ys); break;
-    case FALQON_ACT_GELU_ERF: epilogue_slab<FALQON_ACT_GELU_ERF>(r, alpha, lane, bias, res, zs, ys); break;
-    case FALQON_ACT_GELU_TANH: epilogue_slab<FALQON_ACT_GELU_TANH>(r, alpha, lane, bias, res, zs, ys); break;
-    case FALQON_ACT_SILU: epilogue_slab<FALQON_ACT_SILU>(r, alpha, lane, bias, res, zs, ys); break;
+    case FALQON_ACT_NONE: epilogue_slab<FALQON_ACT_NONE>(r, alpha, bias, has_res, res, z, y, cols, wide); break;
+    case FALQON_ACT_RELU: epilogue_slab<FALQON_ACT_RELU>(r, alpha, bias, has_res, res, z, y, cols, wide); break;
+    case FALQON_ACT_GELU_ERF: epilogue_slab<FALQON_ACT_GELU_ERF>(r, alpha, bias, has_res, res, z, y, cols, wide); break;
+    case FALQON_ACT_GELU_TANH: epilogue_slab<FALQON_ACT_GELU_TANH>(r, alpha, bias, has_res, res, z, y, cols, wide); break;
+    case FALQON_ACT_SILU: epilogue_slab<FALQON_ACT_SILU>(r, alpha, bias, has_res, res, z, y, cols, wide); break;
   }
 }
-
-// The tensor maps of the epilogue's matrices (boxes of one slab).
-struct EpiMaps {
-  CUtensorMap y, z, res;
-};
-struct NoMaps {};
 
 template <bool kBMn, uint32_t kAFmt, int kStages, bool kEpi = false>
 struct PairCfg {
@@ -135,11 +139,7 @@ struct PairCfg {
   static constexpr int WaiterWarp = 2 + EpiWarps;
   static constexpr int Threads = 32 * (WaiterWarp + 1);
   static constexpr int BarBytes = 8 * (2 * kStages + 2 * Acc + 1) + 16;
-  // kEpi, per epilogue warp: two residual slabs, a Z slab and a Y slab (two Y
-  // slabs in turn without Z), the slab's biases, and two barriers of the
-  // residual's loads
-  static constexpr int WarpSlabs = 4;
-  static constexpr int EpiBytes = kEpi ? EpiWarps * (WarpSlabs * kSlabBytes + kSlab * 4 + 16) : 0;
+  static constexpr int EpiBytes = kEpi ? EpiWarps * kSlab * 4 : 0;  // a slab's biases, per epilogue warp
   static constexpr int SmemBytes = kStages * StageBytes + EpiBytes + BarBytes + 1024;
   static constexpr uint32_t IDesc = idesc_f32acc(kAFmt, 0u, 0u, kBMn ? 1u : 0u, 256, TileN);
   static constexpr uint32_t IDescHalf = idesc_f32acc(kAFmt, 0u, 0u, kBMn ? 1u : 0u, 256, TileN / 2);
@@ -149,12 +149,11 @@ struct PairCfg {
 template <class C>
 __global__ void __launch_bounds__(C::Threads, 1)
     tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmBh, const PairArgs g,
-                        const __grid_constant__ std::conditional_t<C::Epi, EpiMaps, NoMaps> em) {
+                        const __grid_constant__ CUtensorMap tmBh, const PairArgs g) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* slabs = smem + C::Stages * C::StageBytes;  // [EpiWarps][WarpSlabs] (kEpi)
+  float* slab_bias = reinterpret_cast<float*>(smem + C::Stages * C::StageBytes);  // [EpiWarps][kSlab] (kEpi)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::Stages * C::StageBytes + C::EpiBytes);
   uint64_t* full = bars;                      // [Stages] both CTAs' tiles landed (even CTA's copy is used)
   uint64_t* empty = bars + C::Stages;         // [Stages] the MMAs are done with this CTA's slot
@@ -192,13 +191,6 @@ __global__ void __launch_bounds__(C::Threads, 1)
       mbar_init(&acc_empty[b], 2 * C::EpiWarps);
     }
     mbar_init(drain, 1);
-    if constexpr (C::Epi) {
-      uint64_t* landed = reinterpret_cast<uint64_t*>(slabs + C::EpiWarps * (C::WarpSlabs * kSlabBytes + kSlab * 4));
-      for (int i = 0; i < 2 * C::EpiWarps; ++i) mbar_init(&landed[i], 1);
-      tma_prefetch_desc(&em.y);
-      if (g.epi.z) tma_prefetch_desc(&em.z);
-      if (g.epi.residual) tma_prefetch_desc(&em.res);
-    }
     *abort_flag = 0;
     fence_barrier_init();  // visible to the other CTA's copies and arrivals
     tma_prefetch_desc(&tmA);
@@ -337,70 +329,59 @@ __global__ void __launch_bounds__(C::Threads, 1)
     }
     if constexpr (C::Epi) {
       const int half = (warp - 2) >> 2;  // this warp takes every other slab of its quarter
-      uint8_t* own = slabs + (warp - 2) * C::WarpSlabs * kSlabBytes;
-      uint8_t* out = own + 2 * kSlabBytes;
-      float* biases = reinterpret_cast<float*>(slabs + C::EpiWarps * C::WarpSlabs * kSlabBytes) + (warp - 2) * kSlab;
-      uint64_t* landed =
-          reinterpret_cast<uint64_t*>(slabs + C::EpiWarps * (C::WarpSlabs * kSlabBytes + kSlab * 4)) + 2 * (warp - 2);
-      const bool has_res = g.epi.residual != nullptr, has_z = g.epi.z != nullptr;
+      float* biases = slab_bias + (warp - 2) * kSlab;
+      const __nv_bfloat16* residual = static_cast<const __nv_bfloat16*>(g.epi.residual);
+      __nv_bfloat16* zmat = static_cast<__nv_bfloat16*>(g.epi.z);
+      __nv_bfloat16* ymat = static_cast<__nv_bfloat16*>(g.out);
       // slab i of this warp in work item w: its place, and whether any of it exists
-      auto place = [&](int w, int i, int& row0, int& col) {
+      auto place = [&](int w, int i, int64_t& row0, int64_t& col) {
         int mt, nt, nh;
         item(w, mt, nt, nh);
-        row0 = mt * C::TileM + static_cast<int>(rank) * kBM + q * 32;
-        col = nt * C::TileN + (nh > 0 ? C::TileN / 2 : 0) + (2 * i + half) * kSlab;
+        row0 = static_cast<int64_t>(mt) * C::TileM + rank * kBM + q * 32;
+        col = static_cast<int64_t>(nt) * C::TileN + (nh > 0 ? C::TileN / 2 : 0) + (2 * i + half) * kSlab;
         return row0 < g.M && col < g.N;
       };
       auto slab_count = [&](int w) { return (w >= g.n_full ? C::TileN / 2 : C::TileN) / kSlab / 2; };
-      // the residual's slabs are fetched in the order of use into two buffers in turn
+      // The next slab's bias (this lane's column) and residual (this lane's
+      // row) are read while the slab before it is worked on.
       int pw = pair, pi = 0;
-      uint32_t fetched = 0, used = 0;
-      auto fetch = [&]() {
+      float bias = 0.0f;
+      uint32_t res[16] = {};
+      auto prefetch = [&]() {
         while (pw < total) {
-          int row0, col;
+          int64_t row0, col;
           const bool there = place(pw, pi, row0, col);
           if (++pi == slab_count(pw)) {
             pi = 0;
             pw += npairs;
           }
           if (!there) continue;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&landed[fetched & 1u], kSlabBytes);
-            tma_load_2d(own + (fetched & 1u) * kSlabBytes, &em.res, &landed[fetched & 1u], col, row0);
+          if (g.epi.bias && col + lane < g.N) bias = load_param(g.epi.bias, g.epi.bias_bf16, col + lane, 0.0f);
+          if (residual && row0 + lane < g.M) {
+            const __nv_bfloat16* p = residual + (row0 + lane) * g.ldo + col;
+            uint32_t h[8];
+            load_global_32B(p, g.wide, h);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) res[k] = h[k];
+            if (col + 16 < g.N) {
+              load_global_32B(p + 16, g.wide, h);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) res[8 + k] = h[k];
+            }
           }
-          ++fetched;
           return;
         }
       };
-      // the bias of this lane's column of the next slab
-      int bw = pair, bi = 0;
-      auto next_bias = [&]() {
-        while (bw < total) {
-          int row0, col;
-          const bool there = place(bw, bi, row0, col);
-          if (++bi == slab_count(bw)) {
-            bi = 0;
-            bw += npairs;
-          }
-          if (there) return g.epi.bias && col + lane < g.N ? load_param(g.epi.bias, g.epi.bias_bf16, col + lane, 0.0f) : 0.0f;
-        }
-        return 0.0f;
-      };
-      if (has_res) {
-        fetch();
-        fetch();
-      }
-      float bias = next_bias();
+      prefetch();
       int acc = 0;
-      uint32_t acc_phase = 0, turn = 0;
-      bool ok = true;
-      for (int w = pair; w < total && ok; w += npairs) {
+      uint32_t acc_phase = 0;
+      for (int w = pair; w < total; w += npairs) {
         if (!warp_wait(&acc_full[acc], acc_phase, abort_flag)) { if (lane == 0) fail(); break; }
         tc_fence_after();
         const int n = slab_count(w);
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-          int row0, col;
+          int64_t row0, col;
           const bool there = place(w, i, row0, col);
           uint32_t r[32];
           if (there) {
@@ -415,44 +396,20 @@ __global__ void __launch_bounds__(C::Threads, 1)
             if (lane == 0) mbar_arrive_cluster(empty_lead + 8u * static_cast<uint32_t>(acc));
           }
           if (!there) continue;
-          const uint8_t* res = nullptr;
-          if (has_res) {
-            if (!warp_wait(&landed[used & 1u], (used >> 1) & 1u, abort_flag)) {
-              if (lane == 0) fail();
-              ok = false;
-              break;
-            }
-            res = own + (used & 1u) * kSlabBytes;
-          }
-          biases[lane] = bias;  // every lane is past the last slab's
-          bias = next_bias();
-          // the stores that read these buffers last are done reading them
-          if (lane == 0) {
-            if (has_z) bulk_wait_read<0>();
-            else bulk_wait_read<1>();
-          }
+          __syncwarp();  // every lane is past the last slab's biases
+          biases[lane] = bias;
+          uint32_t now[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) now[k] = res[k];
+          prefetch();
           __syncwarp();
-          uint8_t* ys = out + (has_z ? kSlabBytes : (turn & 1u) * kSlabBytes);
-          epilogue_slab(g.epi.act, r, alpha, lane, biases, res, has_z ? out : nullptr, ys);
-          fence_proxy_async_smem();  // the slabs are visible to the bulk stores
-          __syncwarp();
-          if (lane == 0) {
-            if (has_z) tma_store_2d(&em.z, out, col, row0);
-            tma_store_2d(&em.y, ys, col, row0);
-            bulk_commit();
-          }
-          ++turn;
-          if (has_res) {  // every lane has read its row of the slab
-            ++used;
-            fetch();
-          }
+          const int64_t at = (row0 + lane) * g.ldo + col;
+          const bool in = row0 + lane < g.M;
+          epilogue_slab(g.epi.act, r, alpha, biases, residual != nullptr, now, in && zmat ? zmat + at : nullptr,
+                        in ? ymat + at : nullptr, static_cast<int>(g.N - col < kSlab ? g.N - col : kSlab), g.wide);
         }
         if (++acc == C::Acc) { acc = 0; acc_phase ^= 1; }
       }
-      // after an abort: what was fetched and not used has landed before the memory goes
-      for (; used < fetched; ++used) mbar_wait_budget(&landed[used & 1u], (used >> 1) & 1u);
-      if (lane == 0) bulk_wait_read<0>();  // the stores no longer read this CTA's memory
-      __syncwarp();
     } else {
       int acc = 0;
       uint32_t acc_phase = 0;
@@ -509,7 +466,7 @@ __global__ void __launch_bounds__(C::Threads, 1)
 using PairFwdCfg = PairCfg<false, 0u, 6>;
 using PairDxCfg = PairCfg<true, 0u, 6>;
 using PairDxE5Cfg = PairCfg<true, 1u, 6>;  // dYq in E5M2
-using PairEpiCfg = PairCfg<false, 0u, 5, true>;
+using PairEpiCfg = PairCfg<false, 0u, 6, true>;
 
 // Pairs the device can keep resident at once (cached per device): the grid
 // never exceeds it, so the persistent pairs all run in one wave.
@@ -565,14 +522,6 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
     if (!make_tmap_2d(&tB, U8, 1, b, Kc, Ncols, C::BK, C::TileN / 2, true)) return cudaErrorInvalidValue;
     if (!make_tmap_2d(&tBh, U8, 1, b, Kc, Ncols, C::BK, C::TileN / 4, true)) return cudaErrorInvalidValue;
   }
-  std::conditional_t<C::Epi, EpiMaps, NoMaps> em{};
-  if constexpr (C::Epi) {
-    const auto B16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    if (!make_tmap_2d_sw64(&em.y, B16, 2, out, Ncols, M, kSlab, kSlab)) return cudaErrorInvalidValue;
-    if (epi.z && !make_tmap_2d_sw64(&em.z, B16, 2, epi.z, Ncols, M, kSlab, kSlab)) return cudaErrorInvalidValue;
-    if (epi.residual && !make_tmap_2d_sw64(&em.res, B16, 2, epi.residual, Ncols, M, kSlab, kSlab))
-      return cudaErrorInvalidValue;
-  }
   PairArgs g{};
   g.m_tiles = ceil_div(M, C::TileM);
   g.n_tiles = ceil_div(Ncols, C::TileN);
@@ -585,6 +534,8 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
   g.scale_b = sb;
   g.dev_status = dev_status;
   g.epi = epi;
+  g.wide = ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(epi.z) |
+             reinterpret_cast<uintptr_t>(epi.residual)) & 31u) == 0;
   const int tiles = g.m_tiles * g.n_tiles;
   if (tiles == 0) return cudaSuccess;
   const int slots = resident_pairs<C>(di);
@@ -598,7 +549,7 @@ cudaError_t pair_gemm(const uint8_t* a, const float* sa, const uint8_t* b, const
     g.n_half = 2 * tail;
   }
   return launch_pdl(tc_gemm_pair_kernel<C>, dim3(static_cast<unsigned>(2 * pairs)), dim3(C::Threads), C::SmemBytes,
-                    stream, 2u, tA, tB, tBh, g, em);
+                    stream, 2u, tA, tB, tBh, g);
 }
 
 }  // namespace
