@@ -563,6 +563,9 @@ cudaError_t launch_fp8_gemm_fwd_pair(const uint8_t* xq, const float* s_x, const 
 cudaError_t launch_fp8_gemm_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
                                          int64_t M, int64_t N, int64_t K, const LinearEpilogue& epi, void* y,
                                          int32_t* dev_status, cudaStream_t stream) {
+  bool taken = false;
+  cudaError_t e = launch_fp8_gemm_fwd_few(xq, s_x, wq, s_w, M, N, K, epi, y, dev_status, stream, &taken);
+  if (e != cudaSuccess || taken) return e;
   return pair_gemm<PairEpiCfg>(xq, s_x, wq, s_w, M, N, K, y, dev_status, stream, epi);
 }
 

@@ -216,6 +216,12 @@ struct LinearEpilogue {
 cudaError_t launch_fp8_gemm_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
                                          int64_t M, int64_t N, int64_t K, const LinearEpilogue& epi, void* y,
                                          int32_t* dev_status, cudaStream_t stream);
+// The same for few rows (gemm_few.cu): 128 x (16 .. 128) tiles, K split over a
+// cluster.  Launches nothing and leaves *taken false where it expects the SM
+// pairs to be faster.
+cudaError_t launch_fp8_gemm_fwd_few(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                                    int64_t M, int64_t N, int64_t K, const LinearEpilogue& epi, void* y,
+                                    int32_t* dev_status, cudaStream_t stream, bool* taken);
 // dz = bf16(dy act'(z)) (nullable), dbias = column sums of the float32 products (nullable).
 size_t epilogue_bwd_workspace_bytes(int64_t M, int64_t N);
 cudaError_t launch_epilogue_bwd(const void* dy, const void* z, falqon_act act, int64_t M, int64_t N, void* dz,

@@ -602,7 +602,10 @@ FALQON_API falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_d
  *
  *   Z = Xq . Wq^T / (s_X s_W) + bias,   Y = bf16( act(Z) + residual )
  * in float32 from the accumulators on, rounded once; z, when wanted, receives
- * bf16(Z) for the backward.
+ * bf16(Z) for the backward.  The order of the float32 sums over K depends on
+ * the sizes alone (few rows split K over several SMs), so the same call gives
+ * the same bits, but Y without any of the three parts may differ from
+ * falqon_linear_fwd's in the last bit.
  *
  *  xq, s_x, wq, s_w as falqon_linear_fwd.  bias [N] in bias_dtype, nullable.
  *  residual [M, N] bfloat16, nullable; it may not be y or z.

@@ -94,12 +94,18 @@ def test_forward(cuda_device, M, N, K, which):
 
 @pytest.mark.parametrize("M,N,K", [(300, 208, 144), (512, 1040, 640), (4736, 1280, 256)])
 def test_nothing_in_the_epilogue_is_the_plain_forward(cuda_device, M, N, K):
-    """At sizes of many rows both run the same products in the same order: the same bits."""
+    """The same product; where both run 256 x 256 tiles the same bits, else float32 sums in another order: each is
+    within (K + 8) 2^-23 of its terms' sizes and half a step of bf16."""
     g = torch.Generator(device="cuda").manual_seed(M)
     xq, s_x = _codes(g, (M, K), 1.0)
     wq, s_w = _codes(g, (N, K), 0.02)
     y, _ = F.falqon_linear_fwd_epilogue(xq, s_x, wq, s_w)
-    assert torch.equal(y, F.falqon_linear_fwd(xq, s_x, wq, s_w))
+    plain = F.falqon_linear_fwd(xq, s_x, wq, s_w)
+    if M > 4096:
+        assert torch.equal(y, plain)
+    mag = block.decode_e4m3(xq).abs() @ block.decode_e4m3(wq).abs().T / (s_x.item() * s_w.item())
+    tol = 2 * ((K + 8) * 2 * E * mag + U * plain.double().abs()) * (1 + U)
+    assert ((y.double() - plain.double()).abs() <= tol).all()
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 16, 16), (1, 4096, 4096), (3, 176, 11008), (33, 4096, 2064), (64, 1040, 4096),
