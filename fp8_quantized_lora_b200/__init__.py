@@ -103,7 +103,7 @@ def lib():
     L.falqon_linear_fwd_grouped.restype = C.c_int
     f32 = C.c_float
     L.falqon_norm_fwd.argtypes = [p, C.c_int, p, p, C.c_int, C.c_int, i64, i64, f32, p, p, p, p, p]
-    L.falqon_norm_bwd.argtypes = [p, p, C.c_int, p, C.c_int, C.c_int, p, p, p, i64, i64, p, p, p, p, sz, p]
+    L.falqon_norm_bwd.argtypes = [p, p, C.c_int, p, C.c_int, C.c_int, p, p, p, i64, i64, p, p, p, p, p, sz, p]
     L.falqon_linear_fwd_epilogue.argtypes = [p, p, p, p, p, C.c_int, C.c_int, p, i64, i64, i64, p, p, p, p]
     L.falqon_linear_epilogue_bwd.argtypes = [p, p, C.c_int, i64, i64, p, p, p, sz, p]
     L.falqon_clip_grads.argtypes = [C.c_int, p, p, p, f32, f32, p, p, p, p, p, sz, p]
@@ -574,7 +574,7 @@ def falqon_norm_fwd(x, gamma=None, beta=None, eps=1e-5, kind=NORM_LAYER, y=True,
 
 
 def falqon_norm_bwd(dy, x, gamma, mean, rstd, kind=NORM_LAYER, dres=None, dx=True, dgamma=True, dbeta=True,
-                    workspace=None, stream=None):
+                    dev_status=None, workspace=None, stream=None):
     """Backward of falqon_norm_fwd; dres (nullable) joins dx.  Each output may
     be True (allocate), a tensor, or None; dgamma and dbeta are float32 sums,
     dbeta is None for NORM_RMS.  Returns (dx, dgamma, dbeta)."""
@@ -598,7 +598,7 @@ def falqon_norm_bwd(dy, x, gamma, mean, rstd, kind=NORM_LAYER, dres=None, dx=Tru
         st = lib().falqon_norm_bwd(_ptr(dy), _ptr(x), _DTYPES[x.dtype], _ptr(gamma),
                                    DTYPE_BF16 if gamma is None else _DTYPES[gamma.dtype], int(kind), _ptr(mean),
                                    _ptr(rstd), _ptr(dres), rows, cols, _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-                                   _ptr(ws), wsb, _stream(stream, dev))
+                                   _ptr(dev_status), _ptr(ws), wsb, _stream(stream, dev))
     _check(st, "falqon_norm_bwd")
     return dx, dgamma, dbeta
 

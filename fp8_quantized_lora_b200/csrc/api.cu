@@ -602,7 +602,7 @@ falqon_status falqon_norm_fwd(const void* x, falqon_dtype dtype, const void* gam
 falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_dtype dtype, const void* gamma,
                               falqon_dtype param_dtype, falqon_norm kind, const float* mean, const float* rstd,
                               const void* dres, int64_t rows, int64_t cols, void* dx, float* dgamma, float* dbeta,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              int32_t* dev_status, void* workspace, size_t workspace_bytes, void* stream) {
   if (!dx && !dgamma && !dbeta) return FALQON_ERR_INVALID_ARG;
   if (!dy || !x || !rstd) return FALQON_ERR_INVALID_ARG;
   falqon_status s = norm_shape(dtype, param_dtype, kind, rows, cols);
@@ -619,7 +619,7 @@ falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_dtype dtype,
   if (!current_device_info()) return FALQON_ERR_CUDA;
   return from_cuda(launch_norm_bwd(dy, x, dtype == FALQON_DTYPE_BF16, gamma, param_dtype == FALQON_DTYPE_BF16,
                                    kind == FALQON_NORM_RMS, mean, rstd, dres, rows, cols, dx, dgamma, dbeta,
-                                   workspace, static_cast<cudaStream_t>(stream)));
+                                   dev_status, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 falqon_status falqon_linear_fwd_epilogue(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,

@@ -10,6 +10,34 @@
 
 namespace falqon {
 
+// Two float32 operations in one instruction (each rounded as its scalar form).
+__device__ __forceinline__ uint64_t f2_bits(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 f2_of(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // Elements of one 16-byte vector.
 template <bool kBF16>
 constexpr int kVec = kBF16 ? 8 : 4;
@@ -51,6 +79,63 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[kVec<kBF16>]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// kBytes (2, 4, 8 or 16) of a row: its words, and the values they hold.
+template <int kBytes>
+struct Words {
+  static constexpr int N = kBytes < 4 ? 1 : kBytes / 4;
+  uint32_t w[N];
+};
+
+template <int kBytes>
+__device__ __forceinline__ Words<kBytes> load_words(const void* p) {
+  Words<kBytes> r;
+  if constexpr (kBytes == 16) {
+    const uint4 q = *static_cast<const uint4*>(p);
+    r.w[0] = q.x; r.w[1] = q.y; r.w[2] = q.z; r.w[3] = q.w;
+  } else if constexpr (kBytes == 8) {
+    const uint2 q = *static_cast<const uint2*>(p);
+    r.w[0] = q.x; r.w[1] = q.y;
+  } else if constexpr (kBytes == 4) {
+    r.w[0] = *static_cast<const uint32_t*>(p);
+  } else {
+    r.w[0] = *static_cast<const uint16_t*>(p);
+  }
+  return r;
+}
+
+template <int kBytes>
+__device__ __forceinline__ void store_words(void* p, const Words<kBytes>& r) {
+  if constexpr (kBytes == 16) *static_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  else if constexpr (kBytes == 8) *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+  else if constexpr (kBytes == 4) *static_cast<uint32_t*>(p) = r.w[0];
+  else *static_cast<uint16_t*>(p) = static_cast<uint16_t>(r.w[0]);
+}
+
+// Values in kBytes of bf16 or float32.
+template <bool kBF16, int kBytes>
+constexpr int kValues = kBytes / (kBF16 ? 2 : 4);
+
+template <bool kBF16, int kBytes>
+__device__ __forceinline__ void values_of(const Words<kBytes>& r, float (&v)[kValues<kBF16, kBytes>]) {
+#pragma unroll
+  for (int j = 0; j < kValues<kBF16, kBytes>; ++j) {
+    if constexpr (!kBF16) v[j] = __uint_as_float(r.w[j]);
+    else v[j] = __uint_as_float(j & 1 ? r.w[j / 2] & 0xFFFF0000u : r.w[j / 2] << 16);
+  }
+}
+
+template <bool kBF16, int kBytes>
+__device__ __forceinline__ Words<kBytes> words_of(const float (&v)[kValues<kBF16, kBytes>]) {
+  Words<kBytes> r;
+#pragma unroll
+  for (int j = 0; j < Words<kBytes>::N; ++j) {
+    if constexpr (!kBF16) r.w[j] = __float_as_uint(v[j]);
+    else if constexpr (kBytes == 2) r.w[j] = pack2(v[0], 0.0f);
+    else r.w[j] = pack2(v[2 * j], v[2 * j + 1]);
+  }
+  return r;
+}
+
 template <bool kBF16>
 __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
   if constexpr (kBF16)
@@ -71,6 +156,29 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
 __device__ __forceinline__ float load_param(const void* p, bool bf16, int64_t i, float none) {
   if (!p) return none;
   return bf16 ? load_elem<true>(p, i) : load_elem<false>(p, i);
+}
+
+// kN consecutive parameters from element i on (a multiple of kN; the vector is
+// 16-byte aligned).
+template <int kN>
+__device__ __forceinline__ void load_params(const void* p, bool bf16, int64_t i, float none, float (&v)[kN]) {
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < kN; ++j) v[j] = none;
+  } else if (bf16) {
+    values_of<true, 2 * kN>(load_words<2 * kN>(static_cast<const uint16_t*>(p) + i), v);
+  } else if constexpr (kN == 8) {
+    float a[4], b[4];
+    values_of<false, 16>(load_words<16>(static_cast<const float*>(p) + i), a);
+    values_of<false, 16>(load_words<16>(static_cast<const float*>(p) + i + 4), b);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[j + 4] = b[j];
+    }
+  } else {
+    values_of<false, 4 * kN>(load_words<4 * kN>(static_cast<const float*>(p) + i), v);
+  }
 }
 
 template <class T>

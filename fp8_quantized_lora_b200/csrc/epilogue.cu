@@ -60,20 +60,36 @@ __global__ void __launch_bounds__(32 * kStripWarps)
   }
 }
 
-// out[c] = sum over p of part[p][c], for up to two sums (blockIdx.y).
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ p0, float* __restrict__ o0,
-                                                          const float* __restrict__ p1, float* __restrict__ o1,
-                                                          int parts, int64_t cols) {
+// out[c] = sum over p of part[p][c], for up to two sums (blockIdx.y).  A block
+// takes 32 columns; its 16 warps each add every sixteenth partial row, and the
+// first joins the sixteen.
+constexpr int kSumWarps = 16;
+
+__global__ void __launch_bounds__(32 * kSumWarps)
+    column_sums_kernel(const float* __restrict__ p0, float* __restrict__ o0, const float* __restrict__ p1,
+                       float* __restrict__ o1, int parts, int64_t cols) {
   pdl_trigger();
   pdl_wait();
+  __shared__ float sums[kSumWarps][33];
   const float* p = blockIdx.y ? p1 : p0;
   float* o = blockIdx.y ? o1 : o0;
-  if (!o) return;
-  for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; c < cols;
-       c += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32; c0 < cols; c0 += static_cast<int64_t>(gridDim.x) * 32) {
+    const int64_t c = c0 + lane;
     float s = 0.0f;
-    for (int i = 0; i < parts; ++i) s += p[static_cast<int64_t>(i) * cols + c];
-    o[c] = s;
+    if (c < cols) {
+#pragma unroll 8
+      for (int i = warp; i < parts; i += kSumWarps) s += p[static_cast<int64_t>(i) * cols + c];
+    }
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < cols) {
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kSumWarps; ++w) v += sums[w][lane];
+      o[c] = v;
+    }
+    __syncthreads();
   }
 }
 
@@ -107,9 +123,9 @@ size_t epilogue_bwd_workspace_bytes(int64_t M, int64_t N) {
 
 cudaError_t launch_column_sums(const float* part0, float* out0, const float* part1, float* out1, int parts,
                                int64_t cols, cudaStream_t stream) {
-  const int64_t blocks = (cols + 255) / 256;
+  const int64_t blocks = (cols + 31) / 32;
   return launch_pdl(column_sums_kernel, dim3(static_cast<unsigned>(blocks < 65535 ? blocks : 65535), out1 ? 2u : 1u),
-                    dim3(256), 0, stream, 1u, part0, out0, part1, out1, parts, cols);
+                    dim3(32 * kSumWarps), 0, stream, 1u, part0, out0, part1, out1, parts, cols);
 }
 
 cudaError_t launch_epilogue_bwd(const void* dy, const void* z, falqon_act act, int64_t M, int64_t N, void* dz,

@@ -203,7 +203,8 @@ cudaError_t launch_norm_fwd(const void* x, bool bf16, const void* gamma, const v
                             int32_t* dev_status, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const void* dy, const void* x, bool bf16, const void* gamma, bool param_bf16, bool rms,
                             const float* mean, const float* rstd, const void* dres, int64_t rows, int64_t cols,
-                            void* dx, float* dgamma, float* dbeta, void* workspace, cudaStream_t stream);
+                            void* dx, float* dgamma, float* dbeta, int32_t* dev_status, void* workspace,
+                            cudaStream_t stream);
 
 // Y = bf16(act(Z) + residual), Z = Xq . Wq^T / (s_x s_w) + bias; z (nullable) receives bf16(Z).
 struct LinearEpilogue {

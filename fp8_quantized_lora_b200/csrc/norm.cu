@@ -12,6 +12,8 @@
 // the difference of two moments, so a large common offset costs no digits.
 // Statistics, sums and the parameter gradients are float32; one rounding per
 // output element.
+#include <algorithm>
+
 #include "elem.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -60,6 +62,210 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
+// Sum of a row of per-warp values, zeros past the last (a multiple of four are read).
+__device__ __forceinline__ float sum_warps(const float* r, int warps) {
+  float s = 0.0f;
+  for (int i = 0; i < warps; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(r + i);
+    s += (v.x + v.y) + (v.z + v.w);
+  }
+  return s;
+}
+
+// Asks for [p, p + bytes) of a matrix that ends at `end` to come into L2 (whole
+// 16-byte units; one thread).
+__device__ __forceinline__ void prefetch_l2(const uint8_t* p, int64_t bytes, const uint8_t* end) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(15);
+  uintptr_t b = (reinterpret_cast<uintptr_t>(p) + bytes + 15) & ~static_cast<uintptr_t>(15);
+  const uintptr_t last = reinterpret_cast<uintptr_t>(end) & ~static_cast<uintptr_t>(15);
+  if (b > last) b = last;
+  if (b > a)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(static_cast<uint32_t>(b - a)) : "memory");
+}
+
+// Sum over the threads that share a row (a warp, or the block), in every
+// thread, in an order that depends on their number alone.  Calls of a block
+// alternate between two buffers: a thread that writes one again has passed the
+// barrier of the call between, which every thread reaches after its reads.
+template <bool kWarp>
+__device__ __forceinline__ float row_sum(float v, float (*red)[32], uint32_t& turn) {
+  v = warp_sum(v);
+  if constexpr (!kWarp) {
+    const int lane = threadIdx.x & 31;
+    float* r = red[turn & 1u];
+    ++turn;
+    if (lane == 0) r[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = sum_warps(r, static_cast<int>(blockDim.x >> 5));
+  }
+  return v;
+}
+
+// How a thread's columns lie in its row, in units of pairs: unit k is one access
+// of kBytes, or, where an access holds a single value, two accesses (a pair all
+// the same: the arithmetic goes two to an instruction).
+template <bool kBF16, int kBytes>
+struct Units {
+  static constexpr int V = kValues<kBF16, kBytes>;
+  static constexpr int Span = V > 1 ? V : 2;  // columns of a unit
+  static constexpr int Pairs = Span / 2;
+  static constexpr int Elem = kBF16 ? 2 : 4;
+  static constexpr int Parts = V > 1 ? 1 : 2;
+  Words<kBytes> w[Parts];
+
+  // first column of unit k for thread t of tpr; the second of a pair of accesses is tpr further
+  __device__ static __forceinline__ int column(int t, int k, int tpr) { return V > 1 ? (t + k * tpr) * V : t + 2 * k * tpr; }
+
+  // row: a pointer to the row's first element; c: column(), below cols
+  __device__ __forceinline__ void load(const uint8_t* row, int c, int tpr, int cols) {
+    w[0] = load_words<kBytes>(row + c * Elem);
+    if constexpr (V == 1) {
+      w[1].w[0] = 0u;
+      if (c + tpr < cols) w[1] = load_words<kBytes>(row + (c + tpr) * Elem);
+    }
+  }
+  __device__ __forceinline__ void pairs(float2 (&out)[Pairs]) const {
+    if constexpr (V == 1) {
+      float a[1], b[1];
+      values_of<kBF16, kBytes>(w[0], a);
+      values_of<kBF16, kBytes>(w[Parts - 1], b);
+      out[0] = make_float2(a[0], b[0]);
+    } else {
+      float v[V];
+      values_of<kBF16, kBytes>(w[0], v);
+#pragma unroll
+      for (int j = 0; j < Pairs; ++j) out[j] = make_float2(v[2 * j], v[2 * j + 1]);
+    }
+  }
+  __device__ static __forceinline__ void store(uint8_t* row, int c, int tpr, int cols, const float2 (&p)[Pairs]) {
+    if constexpr (V == 1) {
+      store_elem<kBF16>(row, c, p[0].x);
+      if (c + tpr < cols) store_elem<kBF16>(row, c + tpr, p[0].y);
+    } else {
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < Pairs; ++j) {
+        v[2 * j] = p[j].x;
+        v[2 * j + 1] = p[j].y;
+      }
+      store_words<kBytes>(row + c * Elem, words_of<kBF16, kBytes>(v));
+    }
+  }
+  __device__ static __forceinline__ void params(const void* v, bool bf16, int c, int tpr, int cols, float none,
+                                                float2 (&out)[Pairs]) {
+    if constexpr (V == 1) {
+      out[0] = make_float2(load_param(v, bf16, c, none), c + tpr < cols ? load_param(v, bf16, c + tpr, none) : 0.0f);
+    } else {
+      float a[V];
+      load_params(v, bf16, c, none, a);
+#pragma unroll
+      for (int j = 0; j < Pairs; ++j) out[j] = make_float2(a[2 * j], a[2 * j + 1]);
+    }
+  }
+};
+
+// The row in registers: kNV accesses of kBytes a thread (kCols columns), which
+// also keeps its columns' parameters; the next row is on its way while this
+// one is summed and written.  kWarp: a warp takes a row, else the block does.
+template <bool kBF16, bool kRms, int kBytes, int kCols, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 128 : 1024)
+    norm_fwd_row_kernel(const void* __restrict__ x, const void* __restrict__ gamma, const void* __restrict__ beta,
+                        bool param_bf16, int64_t rows, int64_t cols, float eps, void* __restrict__ y,
+                        float* __restrict__ mean, float* __restrict__ rstd, int32_t* __restrict__ dev_status) {
+  using U = Units<kBF16, kBytes>;
+  constexpr int kN = kCols / U::Span, kPairs = U::Pairs;
+  __shared__ __align__(16) float red[2][32];
+  if (!kWarp && threadIdx.x < 64) red[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
+  if (!kWarp) __syncthreads();
+  pdl_trigger();
+  pdl_wait();
+  const float inv = 1.0f / static_cast<float>(cols);
+  const int ncols = static_cast<int>(cols);
+  const int tpr = kWarp ? 32 : static_cast<int>(blockDim.x);
+  const int t = kWarp ? static_cast<int>(threadIdx.x) & 31 : static_cast<int>(threadIdx.x);
+  const int64_t first = kWarp ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+  const int64_t step = kWarp ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
+  const int64_t rb = cols * U::Elem;
+  uint32_t turn = 0;
+
+  U w[kN], next[kN];
+  auto fetch = [&](int64_t row) {
+    const uint8_t* xr = static_cast<const uint8_t*>(x) + row * rb;
+#pragma unroll
+    for (int k = 0; k < kN; ++k)
+      if (U::column(t, k, tpr) < ncols) next[k].load(xr, U::column(t, k, tpr), tpr, ncols);
+  };
+  if (first < rows) fetch(first);
+  float2 ga[kN][kPairs], be[kRms ? 1 : kN][kPairs];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const int c = U::column(t, k, tpr);
+    if (c < ncols) {
+      U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, ga[k]);
+      if constexpr (!kRms) U::params(beta, param_bf16, c, tpr, ncols, 0.0f, be[k]);
+    }
+  }
+  for (int64_t row = first; row < rows; row += step) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) w[k] = next[k];
+    if (row + step < rows) fetch(row + step);
+    float mu = 0.0f;
+    if constexpr (!kRms) {
+      float2 s = both(0.0f);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        if (U::column(t, k, tpr) < ncols) {
+          float2 v[kPairs];
+          w[k].pairs(v);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) s = add2(s, v[j]);
+        }
+      }
+      mu = row_sum<kWarp>(s.x + s.y, red, turn) * inv;
+    }
+    float2 q = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int c = U::column(t, k, tpr);
+      if (c < ncols) {
+        float2 v[kPairs];
+        w[k].pairs(v);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          if constexpr (!kRms) v[j] = add2(v[j], both(-mu));
+          if constexpr (!kRms && U::V == 1)
+            if (c + tpr >= ncols) v[j].y = 0.0f;  // no column there
+          q = fma2(v[j], v[j], q);
+        }
+      }
+    }
+    const float rs = 1.0f / sqrtf(row_sum<kWarp>(q.x + q.y, red, turn) * inv + eps);
+    if (t == 0) {
+      if (mean && !kRms) mean[row] = mu;
+      if (rstd) rstd[row] = rs;
+      // a NaN or infinity in the row, or sums past float32: rs is then 0 or NaN (infinite: eps = 0, constant row)
+      if (dev_status && !(rs > 0.0f && isfinite(rs) && isfinite(mu))) atomicOr(dev_status, kDevNonfinite);
+    }
+    uint8_t* yr = static_cast<uint8_t*>(y) + row * rb;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int c = U::column(t, k, tpr);
+      if (c < ncols) {
+        float2 v[kPairs];
+        w[k].pairs(v);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          if constexpr (!kRms) v[j] = add2(v[j], both(-mu));
+          v[j] = mul2(v[j], both(rs));
+          if constexpr (kRms) v[j] = mul2(v[j], ga[k][j]);
+          else v[j] = fma2(v[j], ga[k][j], be[k][j]);
+        }
+        U::store(yr, c, tpr, ncols, v);
+      }
+    }
+  }
+}
+
 // Block b owns the rows [b rows / grid, (b + 1) rows / grid) and one row of
 // each partial sum; a thread owns its columns of them.
 template <bool kBF16, bool kRms>
@@ -101,26 +307,351 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Blocks of the backward, each with one partial row of dgamma and dbeta:
-// two per SM of a B200, never more than rows.
-constexpr int64_t kNormParts = 296;
+// ---------------------------------------------------------------- backward: rows in registers
+// A group of threads takes a row at a time, 8 columns (16 for the longest
+// rows) a thread: their parts of dgamma and dbeta stay in registers over all
+// the rows that the group takes, and the next row of x and dy is on its way
+// while this one is worked on.
+//
+// kMode: a block takes a row (0), a group of `tpr` threads (1) or a warp (2);
+// where a block holds several groups it joins their sums at the end.
+constexpr int kMaxGroups = 15;  // a named barrier each beside the block's
+constexpr int kL2Rows = 2;           // rows ahead that are asked for into L2
+
+// Two sums over a warp with the shuffles of one: after the first exchange the
+// lower lanes hold the first value's parts and the upper ones the second's.
+// Lane 0 gets the first sum, lane 16 the second.
+__device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
+  const bool up = lane & 16;
+  float v = (up ? b : a) + __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+template <bool kBF16, bool kRms, int kBytes, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    norm_bwd_row_kernel(const void* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ gamma,
+                        bool param_bf16, const float* __restrict__ mean, const float* __restrict__ rstd,
+                        const void* __restrict__ dres, int64_t rows, int64_t cols, void* __restrict__ dx,
+                        float* __restrict__ part_g, float* __restrict__ part_b, int group_threads) {
+  using U = Units<kBF16, kBytes>;
+  constexpr int kN = kCols / U::Span, kPairs = U::Pairs;
+  constexpr bool kKeep = kAhead;  // gamma in registers
+  constexpr bool kJoin = kMode != 0;
+  // [call][sum][group][warp]: a block's 32 warps, or 16 of each group, zeros past the last
+  constexpr int kRow = kMode == 0 ? 32 : 16 * (kMaxGroups + 1);
+  __shared__ __align__(16) float red[2][2][kRow];
+  __shared__ float merge[kJoin ? kThreads * kCols : 1];
+  if constexpr (kMode != 2) {
+    for (int i = static_cast<int>(threadIdx.x); i < 4 * kRow; i += static_cast<int>(blockDim.x))
+      (&red[0][0][0])[i] = 0.0f;
+    __syncthreads();
+  }
+  pdl_trigger();
+  pdl_wait();
+  const float inv = 1.0f / static_cast<float>(cols);
+  const int lane = threadIdx.x & 31;
+  const int tpr = kMode == 2 ? 32 : kMode == 1 ? group_threads : static_cast<int>(blockDim.x);
+  const int groups = kMode == 0 ? 1 : static_cast<int>(blockDim.x) / tpr;
+  const int group = kMode == 0 ? 0 : static_cast<int>(threadIdx.x) / tpr;
+  const int t = static_cast<int>(threadIdx.x) - group * tpr, warp = t >> 5;
+  const int step = static_cast<int>(gridDim.x) * groups;
+  const int ncols = static_cast<int>(cols);
+  const int64_t rb = cols * U::Elem;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
+  int64_t at = row * rb;
+  uint32_t turn = 0;
+
+  U wx[kN], wd[kN], nx[kN], nd[kN];
+  float nmu = 0.0f, nrs = 0.0f;
+  auto fetch = [&](int64_t r, int64_t from) {
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int c = U::column(t, k, tpr);
+      if (c < ncols) {
+        nx[k].load(static_cast<const uint8_t*>(x) + from, c, tpr, ncols);
+        nd[k].load(static_cast<const uint8_t*>(dy) + from, c, tpr, ncols);
+      }
+    }
+    if constexpr (!kRms) nmu = mean[r];
+    nrs = rstd[r];
+  };
+  if (row < rows) fetch(row, at);
+  float2 ga[kKeep ? kN : 1][kPairs];
+  float2 ag[kN][kPairs], ab[kRms ? 1 : kN][kPairs];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      ag[k][j] = both(0.0f);
+      if constexpr (!kRms) ab[k][j] = both(0.0f);
+    }
+    const int c = U::column(t, k, tpr);
+    if constexpr (kKeep)
+      if (c < ncols) U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, ga[k]);
+  }
+  for (; row < rows; row += step, at += step * rb) {
+    const float mu = nmu, rs = nrs;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      wx[k] = nx[k];
+      wd[k] = nd[k];
+    }
+    if constexpr (kAhead)
+      if (row + step < rows) fetch(row + step, at + step * rb);
+    if (t == 0 && row + kL2Rows * step < rows) {
+      const int64_t far = (row + kL2Rows * step) * rb, all = rows * rb;
+      prefetch_l2(static_cast<const uint8_t*>(x) + far, rb, static_cast<const uint8_t*>(x) + all);
+      prefetch_l2(static_cast<const uint8_t*>(dy) + far, rb, static_cast<const uint8_t*>(dy) + all);
+      if (dres) prefetch_l2(static_cast<const uint8_t*>(dres) + far, rb, static_cast<const uint8_t*>(dres) + all);
+    }
+    float2 s1 = both(0.0f), s2 = both(0.0f);
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int c = U::column(t, k, tpr);
+      if (c < ncols) {
+        float2 xv[kPairs], dv[kPairs], g[kPairs];
+        wx[k].pairs(xv);
+        wd[k].pairs(dv);
+        if constexpr (!kKeep) U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, g);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          if constexpr (kKeep) g[j] = ga[k][j];
+          if constexpr (!kRms) xv[j] = add2(xv[j], both(-mu));
+          const float2 p = mul2(dv[j], mul2(xv[j], both(rs)));
+          ag[k][j] = add2(ag[k][j], p);
+          s2 = fma2(g[j], p, s2);
+          if constexpr (!kRms) {
+            ab[k][j] = add2(ab[k][j], dv[j]);
+            s1 = fma2(g[j], dv[j], s1);
+          }
+        }
+      }
+    }
+    if (dx) {
+      U wr[kN];
+      if (dres) {
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+          if (U::column(t, k, tpr) < ncols)
+            wr[k].load(static_cast<const uint8_t*>(dres) + at, U::column(t, k, tpr), tpr, ncols);
+      }
+      float c1 = 0.0f, c2;
+      if constexpr (kRms) {
+        c2 = warp_sum(s2.x + s2.y);
+      } else {
+        c2 = warp_sum2(s2.x + s2.y, s1.x + s1.y, lane);
+        if constexpr (kMode == 2) {
+          c1 = __shfl_sync(0xFFFFFFFFu, c2, 16);
+          c2 = __shfl_sync(0xFFFFFFFFu, c2, 0);
+        }
+      }
+      if constexpr (kMode != 2) {
+        // One barrier a row: calls alternate between two buffers, so that a
+        // thread that writes one again has passed the barrier of the call
+        // between, which every thread reaches after its reads.
+        float* r = red[turn & 1u][0] + (kMode == 0 ? 0 : 16 * group);
+        ++turn;
+        if (lane == 0) r[warp] = c2;
+        if constexpr (!kRms)
+          if (lane == 16) r[kRow + warp] = c2;
+        if constexpr (kMode == 0) __syncthreads();
+        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+        c2 = sum_warps(r, tpr >> 5);
+        if constexpr (!kRms) c1 = sum_warps(r + kRow, tpr >> 5);
+      }
+      // dx = g dy rs + (x - mu) a + b
+      const float a = -c2 * inv * rs * rs, b = -c1 * inv * rs;
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const int c = U::column(t, k, tpr);
+        if (c < ncols) {
+          float2 xv[kPairs], dv[kPairs], g[kPairs];
+          wx[k].pairs(xv);
+          wd[k].pairs(dv);
+          if constexpr (!kKeep) U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, g);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            if constexpr (kKeep) g[j] = ga[k][j];
+            if constexpr (!kRms) xv[j] = add2(xv[j], both(-mu));
+            const float2 gd = mul2(dv[j], g[j]);
+            dv[j] = kRms ? mul2(gd, both(rs)) : fma2(gd, both(rs), both(b));
+            dv[j] = fma2(xv[j], both(a), dv[j]);
+          }
+          if (dres) {
+            wr[k].pairs(xv);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) dv[j] = add2(dv[j], xv[j]);
+          }
+          U::store(static_cast<uint8_t*>(dx) + at, c, tpr, ncols, dv);
+        }
+      }
+    }
+    if constexpr (!kAhead)
+      if (row + step < rows) fetch(row + step, at + step * rb);
+  }
+  // this block's row of the partial sums
+  auto put = [&](float* part, const float2(*acc)[kPairs]) {
+    float* to = part + static_cast<int64_t>(blockIdx.x) * cols;
+    float* into = kJoin ? merge + group * static_cast<int>(cols) : to;  // groups * cols <= threads * kCols
+    if (kJoin) __syncthreads();                                        // the sum before this one is read
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const int c = U::column(t, k, tpr);
+      if (c < ncols) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          into[c + 2 * j] = acc[k][j].x;
+          if constexpr (U::V > 1) into[c + 2 * j + 1] = acc[k][j].y;
+          else if (c + tpr < ncols) into[c + tpr] = acc[k][j].y;
+        }
+      }
+    }
+    if (kJoin) {
+      __syncthreads();
+      for (int c = static_cast<int>(threadIdx.x); c < cols; c += static_cast<int>(blockDim.x)) {
+        float s = 0.0f;
+        for (int g = 0; g < groups; ++g) s += merge[g * static_cast<int>(cols) + c];
+        to[c] = s;
+      }
+    }
+  };
+  if (part_g) put(part_g, ag);
+  if constexpr (!kRms)
+    if (part_b) put(part_b, ab);
+}
+
+// Blocks of the backward, each with one partial row of dgamma and dbeta: at
+// most one per SM of a B200 (two where the row is too long for the ring),
+// never more than rows.
+constexpr int64_t kNormParts = 444;
 
 int norm_parts(int64_t rows) { return static_cast<int>(rows < kNormParts ? rows : kNormParts); }
 
-template <bool kBF16, bool kRms>
-cudaError_t norm_fwd_t(const void* x, const void* gamma, const void* beta, bool pbf, int64_t rows, int64_t cols,
-                       float eps, void* y, float* mean, float* rstd, int32_t* dev_status, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20));
-  return launch_pdl(norm_fwd_kernel<kBF16, kRms>, dim3(grid), dim3(kRowThreads), 0, stream, 1u, x, gamma, beta, pbf,
-                    rows, cols, eps, y, mean, rstd, dev_status);
+struct FwdArgs {
+  const void *x, *gamma, *beta;
+  bool param_bf16;
+  int64_t rows, cols;
+  float eps;
+  void* y;
+  float *mean, *rstd;
+  int32_t* dev_status;
+  cudaStream_t stream;
+};
+
+template <bool kBF16, bool kRms, int kBytes, int kCols, bool kWarp>
+cudaError_t norm_fwd_row(const DeviceInfo* di, const FwdArgs& a, int threads) {
+  auto kernel = norm_fwd_row_kernel<kBF16, kRms, kBytes, kCols, kWarp>;
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = kWarp ? (a.rows + 3) / 4 : a.rows, most = static_cast<int64_t>(di->sm_count) * (per_sm > 0 ? per_sm : 1);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(threads), 0, a.stream, 1u,
+                    a.x, a.gamma, a.beta, a.param_bf16, a.rows, a.cols, a.eps, a.y, a.mean, a.rstd, a.dev_status);
+}
+
+template <bool kBF16, bool kRms, int kBytes>
+cudaError_t norm_fwd_bytes(const DeviceInfo* di, const FwdArgs& a, bool* taken) {
+  *taken = true;
+  if (a.cols <= 256) return norm_fwd_row<kBF16, kRms, kBytes, 8, true>(di, a, 128);
+  if (a.cols <= 512) return norm_fwd_row<kBF16, kRms, kBytes, 16, true>(di, a, 128);
+  // 16 columns a thread where they and their parameters fit 64 registers (bf16
+  // in whole vectors), else 8: 4096 x 4096 bf16 layer 15.5 against 20.3 us, but
+  // float32 32.1 against 24.1, and 8192 x 1537 bf16 56.7 against 27.2.
+  constexpr bool kWide = kBF16 && (kBytes == 16 || (kRms && kBytes == 4));
+  auto threads = [&](int c) { return static_cast<int>((a.cols + 32 * c - 1) / (32 * c) * 32); };
+  if constexpr (!kWide)
+    if (a.cols <= 8192) return norm_fwd_row<kBF16, kRms, kBytes, 8, false>(di, a, threads(8));
+  if (a.cols <= 16384) return norm_fwd_row<kBF16, kRms, kBytes, 16, false>(di, a, threads(16));
+  *taken = false;
+  return cudaSuccess;
 }
 
 template <bool kBF16, bool kRms>
-cudaError_t norm_bwd_t(const void* dy, const void* x, const void* gamma, bool pbf, const float* mean,
-                       const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx, float* part_g,
-                       float* part_b, cudaStream_t stream) {
-  return launch_pdl(norm_bwd_kernel<kBF16, kRms>, dim3(norm_parts(rows)), dim3(kRowThreads), 0, stream, 1u, dy, x,
-                    gamma, pbf, mean, rstd, dres, rows, cols, dx, part_g, part_b);
+cudaError_t norm_fwd_t(const FwdArgs& a) {
+  const DeviceInfo* di = current_device_info();
+  if (!di) return cudaErrorInvalidDevice;
+  bool taken = false;
+  const int64_t bytes = a.cols * (kBF16 ? 2 : 4);  // every row begins on a multiple of what divides this
+  cudaError_t e = bytes % 16 == 0  ? norm_fwd_bytes<kBF16, kRms, 16>(di, a, &taken)
+                  : bytes % 4 == 0 ? norm_fwd_bytes<kBF16, kRms, 4>(di, a, &taken)
+                                   : norm_fwd_bytes<kBF16, kRms, kBF16 ? 2 : 4>(di, a, &taken);
+  if (e != cudaSuccess || taken) return e;
+  const unsigned grid = static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20));
+  return launch_pdl(norm_fwd_kernel<kBF16, kRms>, dim3(grid), dim3(kRowThreads), 0, a.stream, 1u, a.x, a.gamma, a.beta,
+                    a.param_bf16, a.rows, a.cols, a.eps, a.y, a.mean, a.rstd, a.dev_status);
+}
+
+struct BwdArgs {
+  const void *dy, *x, *gamma;
+  bool param_bf16;
+  const float *mean, *rstd;
+  const void* dres;
+  int64_t rows, cols;
+  void* dx;
+  float *dgamma, *dbeta;
+  float *part_g, *part_b;  // null where dgamma, dbeta are
+  int32_t* dev_status;
+  cudaStream_t stream;
+};
+
+// Rows' partial sums, or, from a single block, the sums themselves.
+void norm_bwd_outputs(BwdArgs& a, int parts) {
+  if (parts == 1) {
+    a.part_g = a.dgamma;
+    a.part_b = a.dbeta;
+  }
+}
+
+template <bool kBF16, bool kRms, int kBytes, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
+cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
+  auto kernel = norm_bwd_row_kernel<kBF16, kRms, kBytes, kCols, kMode, kThreads, kBlocks, kAhead>;
+  const int tpr = kMode == 2 ? 32 : static_cast<int>((a.cols + 32 * kCols - 1) / (32 * kCols) * 32);
+  int groups = kMode == 0 ? 1 : std::min(kThreads / tpr, kMaxGroups);
+  // few rows: one a group
+  const int64_t sms = di->sm_count;
+  if (a.rows < groups * sms) groups = static_cast<int>(std::max<int64_t>(1, (a.rows + sms - 1) / sms));
+  int per_sm = 0;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, groups * tpr, 0);
+  if (e != cudaSuccess) return e;
+  int64_t blocks = std::min((a.rows + groups - 1) / groups, sms * std::max(1, std::min(per_sm, 3)));
+  blocks = std::min<int64_t>(blocks, norm_parts(a.rows));
+  *parts = static_cast<int>(blocks);
+  norm_bwd_outputs(a, *parts);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(groups * tpr), 0, a.stream, 1u, a.dy, a.x,
+                    a.gamma, a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, tpr);
+}
+
+template <bool kBF16, bool kRms, int kBytes>
+cudaError_t norm_bwd_bytes(const DeviceInfo* di, BwdArgs a, int* parts) {
+  if constexpr (kBF16 && kBytes == 16) {
+    if (a.cols <= 256) return norm_bwd_row<kBF16, kRms, kBytes, 8, 2, 256, 1, true>(di, a, parts);
+    if (a.cols <= 512) return norm_bwd_row<kBF16, kRms, kBytes, 16, 2, 256, 2, true>(di, a, parts);
+    if (a.cols <= 4096) return norm_bwd_row<kBF16, kRms, kBytes, 16, 1, 256, 2, true>(di, a, parts);
+    if (a.cols <= 8192) return norm_bwd_row<kBF16, kRms, kBytes, 16, 0, 512, 1, true>(di, a, parts);
+    if (a.cols <= 16384) return norm_bwd_row<kBF16, kRms, kBytes, 16, 0, 1024, 1, false>(di, a, parts);
+  } else {
+    if (a.cols <= 256) return norm_bwd_row<kBF16, kRms, kBytes, 8, 2, 512, 1, true>(di, a, parts);
+    if (a.cols <= 2048) return norm_bwd_row<kBF16, kRms, kBytes, 8, 1, 512, 1, true>(di, a, parts);
+    if (a.cols <= 4096) return norm_bwd_row<kBF16, kRms, kBytes, 8, 0, 512, 1, true>(di, a, parts);
+    if (a.cols <= 8192) return norm_bwd_row<kBF16, kRms, kBytes, 8, 0, 1024, 1, true>(di, a, parts);
+    if (a.cols <= 16384) return norm_bwd_row<kBF16, kRms, kBytes, 16, 0, 1024, 1, false>(di, a, parts);
+  }
+  *parts = norm_parts(a.rows);
+  norm_bwd_outputs(a, *parts);
+  return launch_pdl(norm_bwd_kernel<kBF16, kRms>, dim3(*parts), dim3(kRowThreads), 0, a.stream, 1u, a.dy, a.x, a.gamma,
+                    a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b);
+}
+
+template <bool kBF16, bool kRms>
+cudaError_t norm_bwd_t(const BwdArgs& a, int* parts) {
+  const DeviceInfo* di = current_device_info();
+  if (!di) return cudaErrorInvalidDevice;
+  const int64_t bytes = a.cols * (kBF16 ? 2 : 4);  // every row begins on a multiple of what divides this
+  return bytes % 16 == 0  ? norm_bwd_bytes<kBF16, kRms, 16>(di, a, parts)
+         : bytes % 4 == 0 ? norm_bwd_bytes<kBF16, kRms, 4>(di, a, parts)
+                          : norm_bwd_bytes<kBF16, kRms, kBF16 ? 2 : 4>(di, a, parts);
 }
 
 }  // namespace
@@ -134,21 +665,24 @@ cudaError_t launch_norm_fwd(const void* x, bool bf16, const void* gamma, const v
                             int32_t* dev_status, cudaStream_t stream) {
   auto fn = bf16 ? (rms ? norm_fwd_t<true, true> : norm_fwd_t<true, false>)
                  : (rms ? norm_fwd_t<false, true> : norm_fwd_t<false, false>);
-  return fn(x, gamma, beta, param_bf16, rows, cols, eps, y, mean, rstd, dev_status, stream);
+  return fn(FwdArgs{x, gamma, beta, param_bf16, rows, cols, eps, y, mean, rstd, dev_status, stream});
 }
 
 cudaError_t launch_norm_bwd(const void* dy, const void* x, bool bf16, const void* gamma, bool param_bf16, bool rms,
                             const float* mean, const float* rstd, const void* dres, int64_t rows, int64_t cols,
-                            void* dx, float* dgamma, float* dbeta, void* workspace, cudaStream_t stream) {
+                            void* dx, float* dgamma, float* dbeta, int32_t* dev_status, void* workspace,
+                            cudaStream_t stream) {
   float* pg = static_cast<float*>(workspace);
   float* pb = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + norm_bwd_workspace_bytes(rows, cols) / 2);
   auto fn = bf16 ? (rms ? norm_bwd_t<true, true> : norm_bwd_t<true, false>)
                  : (rms ? norm_bwd_t<false, true> : norm_bwd_t<false, false>);
-  cudaError_t e = fn(dy, x, gamma, param_bf16, mean, rstd, dres, rows, cols, dx, dgamma ? pg : nullptr,
-                     dbeta ? pb : nullptr, stream);
-  if (e != cudaSuccess || (!dgamma && !dbeta)) return e;
-  return launch_column_sums(dgamma ? pg : nullptr, dgamma, dbeta ? pb : nullptr, dbeta, norm_parts(rows), cols,
-                            stream);
+  int parts = 0;
+  cudaError_t e = fn(BwdArgs{dy, x, gamma, param_bf16, mean, rstd, dres, rows, cols, dx, dgamma, dbeta,
+                             dgamma ? pg : nullptr, dbeta ? pb : nullptr, dev_status, stream},
+                     &parts);
+  if (e != cudaSuccess || (!dgamma && !dbeta) || parts == 1) return e;
+  if (!dgamma) return launch_column_sums(pb, dbeta, nullptr, nullptr, parts, cols, stream);
+  return launch_column_sums(pg, dgamma, dbeta ? pb : nullptr, dbeta, parts, cols, stream);
 }
 
 }  // namespace falqon

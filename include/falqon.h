@@ -593,8 +593,8 @@ FALQON_API falqon_status falqon_norm_fwd(const void* x, falqon_dtype dtype, cons
 FALQON_API falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_dtype dtype, const void* gamma,
                                          falqon_dtype param_dtype, falqon_norm kind, const float* mean,
                                          const float* rstd, const void* dres, int64_t rows, int64_t cols, void* dx,
-                                         float* dgamma, float* dbeta, void* workspace, size_t workspace_bytes,
-                                         void* stream);
+                                         float* dgamma, float* dbeta, int32_t* dev_status, void* workspace,
+                                         size_t workspace_bytes, void* stream);
 
 /*
  * falqon_linear_fwd_epilogue - falqon_linear_fwd with a bias, an activation

@@ -50,7 +50,7 @@ def test_norm_bwd_argument_errors():
 
     def call(dy=P, x=P, dt=BF, gamma=P, pt=BF, kind=LAYER, mean=P, rstd=P, dres=P, rows=4, cols=24, dx=P, dgamma=P,
              dbeta=P, ws=P, wsb=1 << 20):
-        return f(dy, x, dt, gamma, pt, kind, mean, rstd, dres, rows, cols, dx, dgamma, dbeta, ws, wsb, None)
+        return f(dy, x, dt, gamma, pt, kind, mean, rstd, dres, rows, cols, dx, dgamma, dbeta, None, ws, wsb, None)
     assert call(dx=None, dgamma=None, dbeta=None) == 1
     assert call(dy=None) == 1 and call(x=None) == 1 and call(rstd=None) == 1 and call(mean=None) == 1
     assert call(dt=7) == 1 and call(pt=7) == 1 and call(kind=5) == 1 and call(rows=0) == 1 and call(cols=-1) == 1
