@@ -54,42 +54,24 @@ __host__ __device__ constexpr float tail_coef(int k) {
                   : 0.0715008602f;
 }
 
-// exp(-z^2 / 2) and erfc(|z| / sqrt 2).
-__device__ __forceinline__ void normal_tail(float z, float& e, float& h) {
-  e = exp2_fast(z * z * (-0.5f * kLog2E));
-  const float t = rcp_fast(fmaf(0.311126984f, fabsf(z), 1.0f));
-  float p = tail_coef(7);
+// t P(t): erfc(|z| / sqrt 2) without its factor exp(-z^2 / 2), for two values.
+__device__ __forceinline__ float2 normal_tail2(float2 z) {
+  const float2 d = fma2(both(0.311126984f), make_float2(fabsf(z.x), fabsf(z.y)), both(1.0f));
+  const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+  float2 p = both(tail_coef(7));
 #pragma unroll
-  for (int k = 6; k >= 0; --k) p = fmaf(p, t, tail_coef(k));
-  h = p * t * e;
+  for (int k = 6; k >= 0; --k) p = fma2(p, t, both(tail_coef(k)));
+  return mul2(p, t);
 }
 
 // Phi(z) from erfc(|z| / sqrt 2).
 __device__ __forceinline__ float normal_cdf(float z, float h) { return z < 0.0f ? 0.5f * h : fmaf(-0.5f, h, 1.0f); }
 
-// -2u log2(e) of the tanh form.
-__device__ __forceinline__ float gelu_exponent(float z, float z2) {
-  return z * fmaf(z2, -kGeluTwoU * kLog2E * kGeluCubic, -kGeluTwoU * kLog2E);
-}
-
-// Where exp overflows to infinity the reciprocal is 0, the limit.
-template <int kAct>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (kAct == FALQON_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-  if constexpr (kAct == FALQON_ACT_GELU_ERF) {
-    float e, h;
-    normal_tail(z, e, h);
-    return z * normal_cdf(z, h);
-  }
-  if constexpr (kAct == FALQON_ACT_GELU_TANH) return z * rcp_fast(1.0f + exp2_fast(gelu_exponent(z, z * z)));
-  if constexpr (kAct == FALQON_ACT_SILU) return z * rcp_fast(1.0f + exp2_fast(-kLog2E * z));
-  return z;
-}
-
-// Two values at once: the same operations, two to an instruction where there is
-// one for two.
+// Two values at once, two operations to an instruction where there is one.
+// Where 2^n overflows to infinity the reciprocal is 0, the limit.
 template <int kAct>
 __device__ __forceinline__ float2 act_value2(float2 z) {
+  if constexpr (kAct == FALQON_ACT_RELU) return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);  // NaN stays
   if constexpr (kAct == FALQON_ACT_GELU_TANH || kAct == FALQON_ACT_SILU) {
     float2 n;
     if constexpr (kAct == FALQON_ACT_SILU)
@@ -101,41 +83,39 @@ __device__ __forceinline__ float2 act_value2(float2 z) {
   }
   if constexpr (kAct == FALQON_ACT_GELU_ERF) {
     const float2 q = mul2(mul2(z, z), both(-0.5f * kLog2E));
-    const float2 d = fma2(both(0.311126984f), make_float2(fabsf(z.x), fabsf(z.y)), both(1.0f));
-    const float2 t = make_float2(rcp_fast(d.x), rcp_fast(d.y));
-    float2 p = both(tail_coef(7));
-#pragma unroll
-    for (int k = 6; k >= 0; --k) p = fma2(p, t, both(tail_coef(k)));
-    const float2 h = mul2(mul2(p, t), make_float2(exp2_fast(q.x), exp2_fast(q.y)));
+    const float2 h = mul2(normal_tail2(z), make_float2(exp2_fast(q.x), exp2_fast(q.y)));
     return mul2(z, make_float2(normal_cdf(z.x, h.x), normal_cdf(z.y, h.y)));
   }
-  return make_float2(act_value<kAct>(z.x), act_value<kAct>(z.y));
+  return z;
 }
 
-// p + zu p (1 - p) for p = 1 / (1 + 2^n): with e = 2^-|n| <= 1 and
-// r = 1 / (1 + e), p is r or e r and p (1 - p) = e r^2, so neither tail
-// cancels or overflows.
-__device__ __forceinline__ float logistic_slope(float n, float zu) {
-  const float e = exp2_fast(-fabsf(n));
-  const float r = rcp_fast(1.0f + e);
-  const float q = e * r;
-  return fmaf(zu * q, r, n > 0.0f ? q : r);
+// Two derivatives at once.  With p = 1 / (1 + 2^n) the sigmoid forms are
+// p + zu p (1 - p) = p (1 + zu (1 - p)); where 2^n overflows p is 0 and so is
+// the product, as in the limit.
+__device__ __forceinline__ float2 logistic_slope2(float2 n, float2 zu) {
+  const float2 d = add2(make_float2(exp2_fast(n.x), exp2_fast(n.y)), both(1.0f));
+  const float2 p = make_float2(rcp_fast(d.x), rcp_fast(d.y));
+  return mul2(p, fma2(zu, fma2(p, both(-1.0f), both(1.0f)), both(1.0f)));
 }
 
 template <int kAct>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (kAct == FALQON_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+__device__ __forceinline__ float2 act_slope2(float2 z) {
+  if constexpr (kAct == FALQON_ACT_RELU) return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
   if constexpr (kAct == FALQON_ACT_GELU_ERF) {
-    float e, h;
-    normal_tail(z, e, h);
-    return fmaf(z * kInvSqrt2Pi, e, normal_cdf(z, h));
+    const float2 q = mul2(mul2(z, z), both(-0.5f * kLog2E));
+    const float2 e = make_float2(exp2_fast(q.x), exp2_fast(q.y));
+    const float2 h = mul2(normal_tail2(z), e);
+    return fma2(mul2(z, both(kInvSqrt2Pi)), e, make_float2(normal_cdf(z.x, h.x), normal_cdf(z.y, h.y)));
   }
   if constexpr (kAct == FALQON_ACT_GELU_TANH) {
-    const float z2 = fminf(z * z, 400.0f);  // past |z| = 20 p is 0 or 1 whatever z: keeps the products finite
-    return logistic_slope(gelu_exponent(z, z2), z * fmaf(z2, 3.0f * kGeluTwoU * kGeluCubic, kGeluTwoU));
+    // past |z| = 20 p is 0 or 1 whatever z: keeps the products finite
+    float2 z2 = mul2(z, z);
+    z2 = make_float2(fminf(z2.x, 400.0f), fminf(z2.y, 400.0f));
+    const float2 n = mul2(z, fma2(z2, both(-kGeluTwoU * kLog2E * kGeluCubic), both(-kGeluTwoU * kLog2E)));
+    return logistic_slope2(n, mul2(z, fma2(z2, both(3.0f * kGeluTwoU * kGeluCubic), both(kGeluTwoU))));
   }
-  if constexpr (kAct == FALQON_ACT_SILU) return logistic_slope(-kLog2E * z, z);
-  return 1.0f;
+  if constexpr (kAct == FALQON_ACT_SILU) return logistic_slope2(mul2(z, both(-kLog2E)), z);
+  return both(1.0f);
 }
 
 }  // namespace falqon

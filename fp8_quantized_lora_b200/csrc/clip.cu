@@ -5,9 +5,11 @@
 //   out  = g (factor coef), rounded once to g's type
 //
 // Bound by HBM: every gradient is read for the norm, read again for the
-// scaling and written.  The tensors are cut into chunks of 4096 elements that
-// the blocks take in turn; a table of the tensors travels in the kernel's
-// parameters, so a call copies nothing to the device and can be captured.
+// scaling and written.  The tensors are cut into chunks of 16 KB; a block takes
+// a run of them, the same one in both kernels, and scales it from its end
+// backwards, so that what the L2 still holds of it is not read from memory
+// again.  A table of the tensors travels in the kernel's parameters, so a call
+// copies nothing to the device and can be captured.
 //
 // Sums: eight (bf16) or four (float32) squares are added in float32, which is
 // exact enough while the sum stays away from the ends of float32's range, and
@@ -23,23 +25,27 @@ namespace falqon {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 4096;    // elements
+constexpr int kClipVecs = 4;        // 16-byte vectors of a thread in a chunk
+constexpr int kClipChunk = kClipThreads * kClipVecs * 16;  // bytes
 constexpr int kClipTensors = 512;   // tensors of one launch
+constexpr int kClipFew = 32;        // the table of a launch of few tensors: its parameters take less time to arrive
 constexpr int kClipBlocks = 592;    // four per SM of a B200
 
+template <int kTensors>
 struct ClipTable {
-  const void* in[kClipTensors];
-  void* out[kClipTensors];
-  int64_t numel[kClipTensors];
-  uint32_t end[kClipTensors];      // chunks up to and including tensor i
-  uint8_t bf16[kClipTensors];
+  const void* in[kTensors];
+  void* out[kTensors];
+  int64_t numel[kTensors];
+  uint32_t end[kTensors];  // chunks up to and including tensor i
+  uint8_t bf16[kTensors];
   int32_t n;
   uint32_t chunks;
 };
-static_assert(sizeof(ClipTable) <= 32000, "kernel parameters");
+static_assert(sizeof(ClipTable<kClipTensors>) <= 32000, "kernel parameters");
 
 // The tensor that chunk c belongs to: the first whose end is past c.
-__device__ __forceinline__ int clip_tensor(const ClipTable& t, uint32_t c) {
+template <int kTensors>
+__device__ __forceinline__ int clip_tensor(const ClipTable<kTensors>& t, uint32_t c) {
   int lo = 0, hi = t.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -47,6 +53,13 @@ __device__ __forceinline__ int clip_tensor(const ClipTable& t, uint32_t c) {
     else lo = mid + 1;
   }
   return lo;
+}
+
+// This block's run of chunks.
+template <int kTensors>
+__device__ __forceinline__ void clip_run(const ClipTable<kTensors>& t, uint32_t& c0, uint32_t& c1) {
+  c0 = static_cast<uint32_t>(static_cast<uint64_t>(t.chunks) * blockIdx.x / gridDim.x);
+  c1 = static_cast<uint32_t>(static_cast<uint64_t>(t.chunks) * (blockIdx.x + 1) / gridDim.x);
 }
 
 // Sum of the squares of one vector: float32 while the sum is in
@@ -64,19 +77,29 @@ __device__ __forceinline__ double square_sum(const float (&v)[kN]) {
   return d;
 }
 
+// Elements [e0, e1) of a tensor, at most a chunk.
 template <bool kBF16>
 __device__ __forceinline__ double chunk_square_sum(const void* p, int64_t e0, int64_t e1) {
   constexpr int kV = kVec<kBF16>;
+  const uint4* v = static_cast<const uint4*>(p) + e0 / kV;  // chunks begin on whole vectors
+  const int n = static_cast<int>(e1 - e0), whole = n / kV;
   double acc = 0.0;
-  const int64_t whole = e0 + (e1 - e0) / kV * kV;
-  for (int64_t e = e0 + threadIdx.x * kV; e < whole; e += kClipThreads * kV) {
-    float v[kV];
-    unpack16<kBF16>(*reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + e * (16 / kV)), v);
-    acc += square_sum(v);
+  uint4 q[kClipVecs];
+#pragma unroll
+  for (int k = 0; k < kClipVecs; ++k)
+    if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole) q[k] = v[threadIdx.x + k * kClipThreads];
+#pragma unroll
+  for (int k = 0; k < kClipVecs; ++k) {
+    if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole) {
+      float f[kV];
+      unpack16<kBF16>(q[k], f);
+      acc += square_sum(f);
+    }
   }
-  if (whole + threadIdx.x < e1) {
-    const double v = load_elem<kBF16>(p, whole + threadIdx.x);
-    acc = fma(v, v, acc);
+  const int tail = whole * kV + static_cast<int>(threadIdx.x);
+  if (tail < n) {
+    const double x = load_elem<kBF16>(p, e0 + tail);
+    acc = fma(x, x, acc);
   }
   return acc;
 }
@@ -84,31 +107,54 @@ __device__ __forceinline__ double chunk_square_sum(const void* p, int64_t e0, in
 template <bool kBF16>
 __device__ __forceinline__ void scale_chunk(const void* p, void* o, int64_t e0, int64_t e1, float by, bool zero) {
   constexpr int kV = kVec<kBF16>;
-  const int64_t whole = e0 + (e1 - e0) / kV * kV;
-  for (int64_t e = e0 + threadIdx.x * kV; e < whole; e += kClipThreads * kV) {
-    float v[kV];
-    unpack16<kBF16>(*reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + e * (16 / kV)), v);
+  const uint4* v = static_cast<const uint4*>(p) + e0 / kV;
+  uint4* to = static_cast<uint4*>(o) + e0 / kV;
+  const int n = static_cast<int>(e1 - e0), whole = n / kV;
+  uint4 q[kClipVecs];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) v[j] = zero ? 0.0f : v[j] * by;
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(o) + e * (16 / kV)) = pack16<kBF16>(v);
+  for (int k = 0; k < kClipVecs; ++k)  // read and written for the last time here
+    if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole) q[k] = __ldcs(v + threadIdx.x + k * kClipThreads);
+#pragma unroll
+  for (int k = 0; k < kClipVecs; ++k) {
+    if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole) {
+      float f[kV];
+      unpack16<kBF16>(q[k], f);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) f[j] = zero ? 0.0f : f[j] * by;
+      __stcs(to + threadIdx.x + k * kClipThreads, pack16<kBF16>(f));
+    }
   }
-  const int64_t e = whole + threadIdx.x;
-  if (e < e1) store_elem<kBF16>(o, e, zero ? 0.0f : load_elem<kBF16>(p, e) * by);
+  const int tail = whole * kV + static_cast<int>(threadIdx.x);
+  if (tail < n) store_elem<kBF16>(o, e0 + tail, zero ? 0.0f : load_elem<kBF16>(p, e0 + tail) * by);
+}
+
+// Chunk c of tensor i: its elements.
+template <int kTensors>
+__device__ __forceinline__ void chunk_elements(const ClipTable<kTensors>& t, int i, uint32_t c, int64_t& e0, int64_t& e1) {
+  const int64_t size = kClipChunk / (t.bf16[i] ? 2 : 4);
+  e0 = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * size;
+  e1 = e0 + size < t.numel[i] ? e0 + size : t.numel[i];
 }
 
 // part[b] = this block's share (added to what an earlier launch of the call
 // left there when `add`).
+template <int kTensors>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_norm_kernel(const __grid_constant__ ClipTable t, double* __restrict__ part, bool add) {
+    clip_norm_kernel(const __grid_constant__ ClipTable<kTensors> t, double* __restrict__ part, bool add) {
   pdl_trigger();
   pdl_wait();
   __shared__ double red[32];
   double acc = 0.0;
-  for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-    const int i = clip_tensor(t, c);
-    const int64_t e0 = static_cast<int64_t>(c - (i ? t.end[i - 1] : 0u)) * kClipChunk;
-    const int64_t e1 = e0 + kClipChunk < t.numel[i] ? e0 + kClipChunk : t.numel[i];
-    acc += t.bf16[i] ? chunk_square_sum<true>(t.in[i], e0, e1) : chunk_square_sum<false>(t.in[i], e0, e1);
+  uint32_t c0, c1;
+  clip_run(t, c0, c1);
+  if (c0 < c1) {
+    int i = clip_tensor(t, c0);
+    for (uint32_t c = c0; c < c1; ++c) {
+      while (t.end[i] <= c) ++i;
+      int64_t e0, e1;
+      chunk_elements(t, i, c, e0, e1);
+      acc += t.bf16[i] ? chunk_square_sum<true>(t.in[i], e0, e1) : chunk_square_sum<false>(t.in[i], e0, e1);
+    }
   }
   acc = block_sum(acc, red);
   if (threadIdx.x == 0) part[blockIdx.x] = add ? part[blockIdx.x] + acc : acc;
@@ -116,8 +162,9 @@ __global__ void __launch_bounds__(kClipThreads)
 
 // Every block joins the partial sums (in the same order) and scales its
 // chunks; block 0 of the call's first launch publishes the results.
+template <int kTensors>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_scale_kernel(const __grid_constant__ ClipTable t, const double* __restrict__ part, int parts,
+    clip_scale_kernel(const __grid_constant__ ClipTable<kTensors> t, const double* __restrict__ part, int parts,
                       float max_norm, float factor, bool scale, float* __restrict__ norm, float* __restrict__ coef,
                       int32_t* __restrict__ dev_status) {
   pdl_trigger();
@@ -136,69 +183,84 @@ __global__ void __launch_bounds__(kClipThreads)
   }
   if (!scale) return;
   const float by = static_cast<float>(static_cast<double>(factor) * c);
-  for (uint32_t k = blockIdx.x; k < t.chunks; k += gridDim.x) {
-    const int i = clip_tensor(t, k);
-    const int64_t e0 = static_cast<int64_t>(k - (i ? t.end[i - 1] : 0u)) * kClipChunk;
-    const int64_t e1 = e0 + kClipChunk < t.numel[i] ? e0 + kClipChunk : t.numel[i];
+  uint32_t c0, c1;
+  clip_run(t, c0, c1);
+  if (c0 >= c1) return;
+  int i = clip_tensor(t, c1 - 1);
+  for (uint32_t k = c1; k-- > c0;) {
+    while (i > 0 && t.end[i - 1] > k) --i;
+    int64_t e0, e1;
+    chunk_elements(t, i, k, e0, e1);
     if (t.bf16[i]) scale_chunk<true>(t.in[i], t.out[i], e0, e1, by, !finite);
     else scale_chunk<false>(t.in[i], t.out[i], e0, e1, by, !finite);
   }
 }
 
 // Fills `t` from tensor `i` on; returns the next tensor.  A launch takes up to
-// kClipTensors tensors that hold elements.
-int clip_table(ClipTable& t, int i, int n, const void* const* grads, void* const* outs, const falqon_dtype* dtypes,
-               const int64_t* numel) {
+// kTensors tensors that hold elements.
+template <int kTensors>
+int clip_table(ClipTable<kTensors>& t, int i, int n, const void* const* grads, void* const* outs,
+               const falqon_dtype* dtypes, const int64_t* numel) {
   t.n = 0;
   t.chunks = 0;
-  for (; i < n && t.n < kClipTensors; ++i) {
+  for (; i < n && t.n < kTensors; ++i) {
     if (numel[i] == 0) continue;
+    const bool bf16 = dtypes[i] == FALQON_DTYPE_BF16;
+    const int64_t size = kClipChunk / (bf16 ? 2 : 4);
     t.in[t.n] = grads[i];
     t.out[t.n] = outs ? outs[i] : nullptr;
     t.numel[t.n] = numel[i];
-    t.bf16[t.n] = dtypes[i] == FALQON_DTYPE_BF16;
-    t.chunks += static_cast<uint32_t>((numel[i] + kClipChunk - 1) / kClipChunk);
+    t.bf16[t.n] = bf16;
+    t.chunks += static_cast<uint32_t>((numel[i] + size - 1) / size);
     t.end[t.n] = t.chunks;
     ++t.n;
   }
   return i;
 }
 
-unsigned clip_grid(const ClipTable& t) {
-  return t.chunks < static_cast<uint32_t>(kClipBlocks) ? (t.chunks ? t.chunks : 1u) : kClipBlocks;
-}
-
-}  // namespace
-
-int64_t clip_chunk_elements() { return kClipChunk; }
-
-size_t clip_workspace_bytes() { return align_up(kClipBlocks * sizeof(double), 256); }
-
-cudaError_t launch_clip_grads(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
-                              float max_norm, float factor, void* const* outs, float* norm, float* coef,
-                              int32_t* dev_status, void* workspace, cudaStream_t stream) {
-  double* part = static_cast<double*>(workspace);
-  ClipTable t;
+template <int kTensors>
+cudaError_t clip_grads_t(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                         float max_norm, float factor, void* const* outs, float* norm, float* coef,
+                         int32_t* dev_status, double* part, cudaStream_t stream) {
+  ClipTable<kTensors> t;
+  auto grid_of = [&]() {
+    return t.chunks < static_cast<uint32_t>(kClipBlocks) ? (t.chunks ? t.chunks : 1u) : static_cast<unsigned>(kClipBlocks);
+  };
   int parts = 0;
   for (int i = 0; i < n || parts == 0;) {  // at least one launch: no elements at all give norm 0
     i = clip_table(t, i, n, grads, outs, dtypes, numel);
     // the first launch sets how many sums there are; later ones add to them
-    const unsigned grid = parts ? static_cast<unsigned>(parts) : (i < n ? kClipBlocks : clip_grid(t));
-    cudaError_t e = launch_pdl(clip_norm_kernel, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts != 0);
+    const unsigned grid = parts ? static_cast<unsigned>(parts) : (i < n ? kClipBlocks : grid_of());
+    cudaError_t e =
+        launch_pdl(clip_norm_kernel<kTensors>, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts != 0);
     if (e != cudaSuccess) return e;
     parts = static_cast<int>(grid);
   }
   bool first = true;
   for (int i = 0; i < n || first;) {
     i = clip_table(t, i, n, grads, outs, dtypes, numel);
-    const unsigned grid = outs ? clip_grid(t) : 1u;
-    cudaError_t e = launch_pdl(clip_scale_kernel, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts,
-                               max_norm, factor, outs != nullptr, first ? norm : nullptr, coef, dev_status);
+    cudaError_t e = launch_pdl(clip_scale_kernel<kTensors>, dim3(outs ? grid_of() : 1u), dim3(kClipThreads), 0, stream,
+                               1u, t, part, parts, max_norm, factor, outs != nullptr, first ? norm : nullptr, coef,
+                               dev_status);
     if (e != cudaSuccess) return e;
     first = false;
     if (!outs) break;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+int64_t clip_chunk_elements() { return kClipChunk / 4; }
+
+size_t clip_workspace_bytes() { return align_up(kClipBlocks * sizeof(double), 256); }
+
+cudaError_t launch_clip_grads(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                              float max_norm, float factor, void* const* outs, float* norm, float* coef,
+                              int32_t* dev_status, void* workspace, cudaStream_t stream) {
+  auto fn = n <= kClipFew ? clip_grads_t<kClipFew> : clip_grads_t<kClipTensors>;
+  return fn(n, grads, dtypes, numel, max_norm, factor, outs, norm, coef, dev_status, static_cast<double*>(workspace),
+            stream);
 }
 
 }  // namespace falqon
