@@ -10,7 +10,6 @@ the built library raises.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -491,60 +490,86 @@ def falqon_lora_separate_bwd(precision, dyq, s_dy, dy, wq, s_w, xq, s_x, x, A, B
 
 
 # ------------------------------------------------------------------ around the linear layer
+# Small calls take the GPU two to five microseconds, so these bindings are
+# written to spend little more on the host: one check per tensor, integers for
+# pointers, no context managers where the tensors' device and stream are
+# current.
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+_CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _on(dev, stream):
-    """Makes `dev` and the caller's stream current, where they are not: what is
-    allocated then belongs to the stream that the call runs on."""
+def _elsewhere(dev, stream):
+    """A scope that makes `dev` and the caller's stream current, or None where
+    they are: what is allocated then belongs to the stream that the call runs on."""
     if stream is not None:
         return torch.cuda.stream(stream)  # also selects the stream's device
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _expect(t, name, shape, dtypes, dev):
-    """The call reads `shape` elements of `dtypes` on `dev` behind this pointer."""
+def _addr(t, name, shape, dtypes, dev):
+    """The address of a tensor that the call takes `shape` elements of `dtypes` at; None for None."""
     if t is None:
-        return
+        return None
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-_F32, _BF16, _EITHER = (torch.float32,), (torch.bfloat16,), (torch.bfloat16, torch.float32)
-_CODES = tuple(getattr(torch, n) for n in ("uint8", "float8_e4m3fn"))
+_F32, _BF16, _EITHER, _I32 = (torch.float32,), (torch.bfloat16,), (torch.bfloat16, torch.float32), (torch.int32,)
 
 
-def _cuda_2d(t, name):
+def _scalar(t, name, dev):
+    """The address of one float (a scale), of any shape."""
+    return _addr(t, name, t.shape if t.numel() == 1 else (1,), _F32, dev)
+
+
+def _device_of(t, name, dtypes):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     if not t.is_cuda:
         raise ValueError("falqon tensors must live on a CUDA device")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    return t.device
 
 
-def _output(v, name, shape, dtype, dev):
-    """An output that may be True (allocate), a tensor, or None (not wanted)."""
+def _like(v, t):
+    """An output with the shape and type of `t`: True (allocate), a tensor, or None (not wanted)."""
     if v is True:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if v is None or v is False:
-        return None
-    _expect(v, name, shape, (dtype,), dev)
-    return v
+        return torch.empty_like(t)
+    return None if v is False else v
+
+
+def _vector(v, n, t):
+    """The same for `n` float32 on the device of `t`."""
+    if v is True:
+        return t.new_empty((n,), dtype=torch.float32)
+    return None if v is False else v
 
 
 def _scratch(op, M, N, K, dev, workspace):
-    """A workspace that needs no initialisation: the caller's, or one of this call."""
-    need = falqon_workspace_size(op, M, N, K, 0)
+    """(tensor, address, bytes) of a workspace that needs no initialisation: the caller's, or one of this call."""
     if workspace is None:
+        need = falqon_workspace_size(op, M, N, K, 0)
         raw = torch.empty(need + 256, dtype=torch.uint8, device=dev)
-        off = (-raw.data_ptr()) % 256
-        return raw[off:off + need], need
-    if workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
-    return workspace, workspace.numel() * workspace.element_size()
+        return raw, raw.data_ptr() + (-raw.data_ptr()) % 256, need
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _status(dev_status, dev):
+    return None if dev_status is None else _addr(dev_status, "dev_status", dev_status.shape, _I32, dev)
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def falqon_norm_fwd(x, gamma=None, beta=None, eps=1e-5, kind=NORM_LAYER, y=True, mean=True, rstd=True,
@@ -553,22 +578,26 @@ def falqon_norm_fwd(x, gamma=None, beta=None, eps=1e-5, kind=NORM_LAYER, y=True,
     cols], bf16 or fp32; returns (y, mean, rstd).  mean and rstd (float32
     [rows], what falqon_norm_bwd reads) may be True (allocate), a tensor, or
     None; mean is None for NORM_RMS."""
-    _cuda_2d(x, "x")
-    rows, cols = x.shape
-    dev = x.device
-    if x.dtype not in _DTYPES:
-        raise ValueError("x must be bfloat16 or float32")
-    _expect(gamma, "gamma", (cols,), _EITHER, dev)
-    _expect(beta, "beta", (cols,), _EITHER if gamma is None else (gamma.dtype,), dev)
+    dev = _device_of(x, "x", _EITHER)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return falqon_norm_fwd(x, gamma, beta, eps, kind, y, mean, rstd, dev_status)
+    shape = x.shape
+    rows, cols = shape
+    dtype = x.dtype
     param = gamma if gamma is not None else beta
-    with _on(dev, stream):
-        y = _output(True if y is None else y, "y", x.shape, x.dtype, dev)
-        mean = _output(None if kind == NORM_RMS and mean is True else mean, "mean", (rows,), torch.float32, dev)
-        rstd = _output(rstd, "rstd", (rows,), torch.float32, dev)
-        st = lib().falqon_norm_fwd(_ptr(x), _DTYPES[x.dtype], _ptr(gamma), _ptr(beta),
-                                   DTYPE_BF16 if param is None else _DTYPES[param.dtype], int(kind), rows, cols,
-                                   float(eps), _ptr(y), _ptr(mean), _ptr(rstd), _ptr(dev_status),
-                                   _stream(stream, dev))
+    pdtypes = _EITHER if param is None else (param.dtype,)
+    if param is not None and param.dtype not in _DTYPES:
+        raise ValueError(f"gamma and beta must be bfloat16 or float32, got {param.dtype}")
+    y = _like(True if y is None else y, x)
+    mean = _vector(None if kind == NORM_RMS and mean is True else mean, rows, x)
+    rstd = _vector(rstd, rows, x)
+    st = lib().falqon_norm_fwd(
+        _addr(x, "x", shape, (dtype,), dev), _DTYPES[dtype], _addr(gamma, "gamma", (cols,), pdtypes, dev),
+        _addr(beta, "beta", (cols,), pdtypes, dev), DTYPE_BF16 if param is None else _DTYPES[param.dtype], kind, rows,
+        cols, eps, _addr(y, "y", shape, (dtype,), dev), _addr(mean, "mean", (rows,), _F32, dev),
+        _addr(rstd, "rstd", (rows,), _F32, dev), _status(dev_status, dev), _raw_stream(dev))
     _check(st, "falqon_norm_fwd")
     return y, mean, rstd
 
@@ -578,27 +607,28 @@ def falqon_norm_bwd(dy, x, gamma, mean, rstd, kind=NORM_LAYER, dres=None, dx=Tru
     """Backward of falqon_norm_fwd; dres (nullable) joins dx.  Each output may
     be True (allocate), a tensor, or None; dgamma and dbeta are float32 sums,
     dbeta is None for NORM_RMS.  Returns (dx, dgamma, dbeta)."""
-    _cuda_2d(x, "x")
-    rows, cols = x.shape
-    dev = x.device
-    if x.dtype not in _DTYPES:
-        raise ValueError("x must be bfloat16 or float32")
-    _expect(dy, "dy", x.shape, (x.dtype,), dev)
-    _expect(dres, "dres", x.shape, (x.dtype,), dev)
-    _expect(gamma, "gamma", (cols,), _EITHER, dev)
-    _expect(mean, "mean", (rows,), _F32, dev)
-    _expect(rstd, "rstd", (rows,), _F32, dev)
-    with _on(dev, stream):
-        dx = _output(dx, "dx", x.shape, x.dtype, dev)
-        dgamma = _output(dgamma, "dgamma", (cols,), torch.float32, dev)
-        dbeta = _output(None if kind == NORM_RMS and dbeta is True else dbeta, "dbeta", (cols,), torch.float32, dev)
-        ws, wsb = (None, 0)
-        if dgamma is not None or dbeta is not None:
-            ws, wsb = _scratch(OP_NORM_BWD, rows, 0, cols, dev, workspace)
-        st = lib().falqon_norm_bwd(_ptr(dy), _ptr(x), _DTYPES[x.dtype], _ptr(gamma),
-                                   DTYPE_BF16 if gamma is None else _DTYPES[gamma.dtype], int(kind), _ptr(mean),
-                                   _ptr(rstd), _ptr(dres), rows, cols, _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-                                   _ptr(dev_status), _ptr(ws), wsb, _stream(stream, dev))
+    dev = _device_of(x, "x", _EITHER)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return falqon_norm_bwd(dy, x, gamma, mean, rstd, kind, dres, dx, dgamma, dbeta, dev_status, workspace)
+    shape = x.shape
+    rows, cols = shape
+    dtype = x.dtype
+    own = (dtype,)
+    dx = _like(dx, x)
+    dgamma = _vector(dgamma, cols, x)
+    dbeta = _vector(None if kind == NORM_RMS and dbeta is True else dbeta, cols, x)
+    ws, wsp, wsb = (None, None, 0)
+    if dgamma is not None or dbeta is not None:
+        ws, wsp, wsb = _scratch(OP_NORM_BWD, rows, 0, cols, dev, workspace)
+    st = lib().falqon_norm_bwd(
+        _addr(dy, "dy", shape, own, dev), _addr(x, "x", shape, own, dev), _DTYPES[dtype],
+        _addr(gamma, "gamma", (cols,), _EITHER, dev), DTYPE_BF16 if gamma is None else _DTYPES[gamma.dtype], kind,
+        _addr(mean, "mean", (rows,), _F32, dev), _addr(rstd, "rstd", (rows,), _F32, dev),
+        _addr(dres, "dres", shape, own, dev), rows, cols, _addr(dx, "dx", shape, own, dev),
+        _addr(dgamma, "dgamma", (cols,), _F32, dev), _addr(dbeta, "dbeta", (cols,), _F32, dev),
+        _status(dev_status, dev), wsp, wsb, _raw_stream(dev))
     _check(st, "falqon_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -608,24 +638,24 @@ def falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias=None, act=ACT_NONE, residu
     """Y = act(Xq . Wq^T / (s_x s_w) + bias) + residual in bf16; returns (y, z).
     z, the pre-activation in bf16 for falqon_linear_epilogue_bwd, may be True
     (allocate), a tensor, or None."""
-    _cuda_2d(xq, "xq")
-    _cuda_2d(wq, "wq")
+    dev = _device_of(xq, "xq", _CODES)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias, act, residual, z, y, dev_status)
+    if wq.dim() != 2:
+        raise ValueError("wq must be 2-D")
     M, K = xq.shape
     N = wq.shape[0]
-    dev = xq.device
-    _expect(xq, "xq", (M, K), _CODES, dev)
-    _expect(wq, "wq", (N, K), _CODES, dev)
-    for t, name in ((s_x, "s_x"), (s_w, "s_w")):
-        _expect(t, name, t.shape if t.numel() == 1 else (1,), _F32, dev)
-    _expect(bias, "bias", (N,), _EITHER, dev)
-    _expect(residual, "residual", (M, N), _BF16, dev)
-    with _on(dev, stream):
-        y = _output(True if y is None else y, "y", (M, N), torch.bfloat16, dev)
-        z = _output(z, "z", (M, N), torch.bfloat16, dev)
-        st = lib().falqon_linear_fwd_epilogue(
-            _ptr(_u8(xq)), _ptr(s_x), _ptr(_u8(wq)), _ptr(s_w), _ptr(bias),
-            DTYPE_BF16 if bias is None else _DTYPES[bias.dtype], int(act), _ptr(residual), M, N, K, _ptr(z), _ptr(y),
-            _ptr(dev_status), _stream(stream, dev))
+    out = (M, N)
+    if y is True or y is None:
+        y = xq.new_empty(out, dtype=torch.bfloat16)
+    z = _like(z, y)
+    st = lib().falqon_linear_fwd_epilogue(
+        _addr(xq, "xq", (M, K), _CODES, dev), _scalar(s_x, "s_x", dev), _addr(wq, "wq", (N, K), _CODES, dev),
+        _scalar(s_w, "s_w", dev), _addr(bias, "bias", (N,), _EITHER, dev),
+        DTYPE_BF16 if bias is None else _DTYPES[bias.dtype], act, _addr(residual, "residual", out, _BF16, dev), M, N, K,
+        _addr(z, "z", out, _BF16, dev), _addr(y, "y", out, _BF16, dev), _status(dev_status, dev), _raw_stream(dev))
     _check(st, "falqon_linear_fwd_epilogue")
     return y, z
 
@@ -634,19 +664,21 @@ def falqon_linear_epilogue_bwd(dy, z, act, dz=True, dbias=True, workspace=None, 
     """dZ = dY act'(Z) in bf16 and dbias, its column sums in float32; each may
     be True (allocate), a tensor, or None.  z may be None for ACT_NONE, whose
     dZ is dY.  Returns (dz, dbias)."""
-    _cuda_2d(dy, "dy")
-    M, N = dy.shape
-    dev = dy.device
-    _expect(dy, "dy", (M, N), _BF16, dev)
-    _expect(z, "z", (M, N), _BF16, dev)
-    with _on(dev, stream):
-        dz = _output(dz, "dz", (M, N), torch.bfloat16, dev)
-        dbias = _output(dbias, "dbias", (N,), torch.float32, dev)
-        ws, wsb = (None, 0)
-        if dbias is not None:
-            ws, wsb = _scratch(OP_LINEAR_EPILOGUE_BWD, M, N, 0, dev, workspace)
-        st = lib().falqon_linear_epilogue_bwd(_ptr(dy), _ptr(z), int(act), M, N, _ptr(dz), _ptr(dbias), _ptr(ws), wsb,
-                                              _stream(stream, dev))
+    dev = _device_of(dy, "dy", _BF16)
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return falqon_linear_epilogue_bwd(dy, z, act, dz, dbias, workspace)
+    shape = dy.shape
+    M, N = shape
+    dz = _like(dz, dy)
+    dbias = _vector(dbias, N, dy)
+    ws, wsp, wsb = (None, None, 0)
+    if dbias is not None:
+        ws, wsp, wsb = _scratch(OP_LINEAR_EPILOGUE_BWD, M, N, 0, dev, workspace)
+    st = lib().falqon_linear_epilogue_bwd(
+        _addr(dy, "dy", shape, _BF16, dev), _addr(z, "z", shape, _BF16, dev), act, M, N,
+        _addr(dz, "dz", shape, _BF16, dev), _addr(dbias, "dbias", (N,), _F32, dev), wsp, wsb, _raw_stream(dev))
     _check(st, "falqon_linear_epilogue_bwd")
     return dz, dbias
 
@@ -687,21 +719,24 @@ def falqon_clip_grads(grads, max_norm, factor=1.0, out=None, norm=None, coef=Non
     (out, norm, coef), norm and coef being float32 [1]."""
     g = grads if isinstance(grads, GradList) else GradList(grads)
     dev = g.device
-    with _on(dev, stream):
-        o = out
-        if out is True:
-            o = GradList(torch.empty_like(t) for t in g)
-        elif out is not None and not isinstance(out, GradList):
-            o = GradList(out)
-        if o is not None and o is not g:
-            if len(o) != len(g) or o.device != dev or bytes(o.numel) != bytes(g.numel) or \
-                    bytes(o.dtypes) != bytes(g.dtypes):
-                raise ValueError("out must match grads in number, sizes, types and device")
-        norm = _output(True if norm is None else norm, "norm", (1,), torch.float32, dev)
-        coef = _output(True if coef is None else coef, "coef", (1,), torch.float32, dev)
-        ws, wsb = _scratch(OP_CLIP_GRADS, 0, 0, 0, dev, workspace)
-        st = lib().falqon_clip_grads(len(g), g.pointers, g.dtypes, g.numel, float(max_norm), float(factor),
-                                     None if o is None else o.pointers, _ptr(norm), _ptr(coef), _ptr(dev_status),
-                                     _ptr(ws), wsb, _stream(stream, dev))
+    scope = _elsewhere(dev, stream)
+    if scope is not None:
+        with scope:
+            return falqon_clip_grads(g, max_norm, factor, g if out is grads else out, norm, coef, dev_status, workspace)
+    o = out
+    if out is True:
+        o = GradList(torch.empty_like(t) for t in g)
+    elif out is not None and not isinstance(out, GradList):
+        o = GradList(out)
+    if o is not None and o is not g:
+        if len(o) != len(g) or o.device != dev or bytes(o.numel) != bytes(g.numel) or \
+                bytes(o.dtypes) != bytes(g.dtypes):
+            raise ValueError("out must match grads in number, sizes, types and device")
+    norm = _vector(True if norm is None else norm, 1, g.tensors[0])
+    coef = _vector(True if coef is None else coef, 1, g.tensors[0])
+    ws, wsp, wsb = _scratch(OP_CLIP_GRADS, 0, 0, 0, dev, workspace)
+    st = lib().falqon_clip_grads(len(g), g.pointers, g.dtypes, g.numel, max_norm, factor,
+                                 None if o is None else o.pointers, _scalar(norm, "norm", dev),
+                                 _scalar(coef, "coef", dev), _status(dev_status, dev), wsp, wsb, _raw_stream(dev))
     _check(st, "falqon_clip_grads")
     return (None if o is None else o.tensors), norm, coef

@@ -540,13 +540,28 @@ struct FwdArgs {
   cudaStream_t stream;
 };
 
+// Resident blocks per SM of a kernel at so many threads (at most 1024; cached:
+// every device of a process is taken to be alike).
+template <class Kernel>
+cudaError_t resident_blocks(Kernel kernel, int threads, int (&cache)[33], int* blocks) {
+  int& slot = cache[threads / 32];
+  *blocks = __atomic_load_n(&slot, __ATOMIC_RELAXED);
+  if (*blocks > 0) return cudaSuccess;
+  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks, kernel, threads, 0);
+  if (e != cudaSuccess) return e;
+  if (*blocks < 1) *blocks = 1;
+  __atomic_store_n(&slot, *blocks, __ATOMIC_RELAXED);
+  return cudaSuccess;
+}
+
 template <bool kBF16, bool kRms, int kBytes, int kCols, bool kWarp>
 cudaError_t norm_fwd_row(const DeviceInfo* di, const FwdArgs& a, int threads) {
   auto kernel = norm_fwd_row_kernel<kBF16, kRms, kBytes, kCols, kWarp>;
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0);
+  static int cache[33] = {};
+  int per_sm = 1;
+  cudaError_t e = resident_blocks(kernel, threads, cache, &per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = kWarp ? (a.rows + 3) / 4 : a.rows, most = static_cast<int64_t>(di->sm_count) * (per_sm > 0 ? per_sm : 1);
+  const int64_t blocks = kWarp ? (a.rows + 3) / 4 : a.rows, most = static_cast<int64_t>(di->sm_count) * per_sm;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(threads), 0, a.stream, 1u,
                     a.x, a.gamma, a.beta, a.param_bf16, a.rows, a.cols, a.eps, a.y, a.mean, a.rstd, a.dev_status);
 }
@@ -612,10 +627,11 @@ cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
   // few rows: one a group
   const int64_t sms = di->sm_count;
   if (a.rows < groups * sms) groups = static_cast<int>(std::max<int64_t>(1, (a.rows + sms - 1) / sms));
-  int per_sm = 0;
-  cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, groups * tpr, 0);
+  static int cache[33] = {};
+  int per_sm = 1;
+  cudaError_t e = resident_blocks(kernel, groups * tpr, cache, &per_sm);
   if (e != cudaSuccess) return e;
-  int64_t blocks = std::min((a.rows + groups - 1) / groups, sms * std::max(1, std::min(per_sm, 3)));
+  int64_t blocks = std::min((a.rows + groups - 1) / groups, sms * std::min(per_sm, 3));
   blocks = std::min<int64_t>(blocks, norm_parts(a.rows));
   *parts = static_cast<int>(blocks);
   norm_bwd_outputs(a, *parts);
