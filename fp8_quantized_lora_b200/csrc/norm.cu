@@ -101,79 +101,120 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], uint32_t& tu
   return v;
 }
 
-// How a thread's columns lie in its row, in units of pairs: unit k is one access
-// of kBytes, or, where an access holds a single value, two accesses (a pair all
-// the same: the arithmetic goes two to an instruction).
-template <bool kBF16, int kBytes>
-struct Units {
-  static constexpr int V = kValues<kBF16, kBytes>;
-  static constexpr int Span = V > 1 ? V : 2;  // columns of a unit
-  static constexpr int Pairs = Span / 2;
+// A thread's columns lie in 16-byte units of memory, whatever the row length: a
+// row whose first element is `shift` elements into a unit (kShift; shift is 0
+// without it) has unit i hold the columns i V - shift .. + V, of which the
+// first and last unit hold some.  Rows a multiple of V apart have the same
+// shift, so a block that takes such rows keeps its columns, their parameters
+// and their sums in registers all the same.
+template <bool kBF16, bool kShift>
+struct Unit {
+  static constexpr int V = kVec<kBF16>;
+  static constexpr int Pairs = V / 2;
   static constexpr int Elem = kBF16 ? 2 : 4;
-  static constexpr int Parts = V > 1 ? 1 : 2;
-  Words<kBytes> w[Parts];
+  uint4 q;
 
-  // first column of unit k for thread t of tpr; the second of a pair of accesses is tpr further
-  __device__ static __forceinline__ int column(int t, int k, int tpr) { return V > 1 ? (t + k * tpr) * V : t + 2 * k * tpr; }
+  __device__ static __forceinline__ int column(int unit, int shift) { return unit * V - (kShift ? shift : 0); }
+  // whether any / every column of the unit at c exists
+  __device__ static __forceinline__ bool some(int c, int cols) { return c < cols; }
+  __device__ static __forceinline__ bool whole(int c, int cols) { return !kShift || (c >= 0 && c + V <= cols); }
+  __device__ static __forceinline__ bool has(int c, int j, int cols) { return !kShift || (c + j >= 0 && c + j < cols); }
 
-  // row: a pointer to the row's first element; c: column(), below cols
-  __device__ __forceinline__ void load(const uint8_t* row, int c, int tpr, int cols) {
-    w[0] = load_words<kBytes>(row + c * Elem);
-    if constexpr (V == 1) {
-      w[1].w[0] = 0u;
-      if (c + tpr < cols) w[1] = load_words<kBytes>(row + (c + tpr) * Elem);
+  // row: the row's first element; end: the matrix's.  A unit that the row
+  // shares with its neighbours is read whole where it lies in the matrix.
+  __device__ __forceinline__ void load(const uint8_t* row, int c, const uint8_t* end) {
+    const uint8_t* p = row + static_cast<int64_t>(c) * Elem;
+    if (!kShift || p + 16 <= end) {
+      q = *reinterpret_cast<const uint4*>(p);
+    } else {  // the matrix's last unit, not a whole one
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = p + (j + 1) * Elem <= end ? load_elem<kBF16>(p, j) : 0.0f;
+      q = pack16<kBF16>(v);
     }
+  }
+  // a unit as loaded, with the columns that are not the row's set to 0 (at its
+  // use: doing it at once would wait for the load)
+  __device__ __forceinline__ Unit trimmed(int c, int cols) const {
+    Unit r = *this;
+    if (!whole(c, cols)) {
+      const uint4 m = mask(c, cols);
+      r.q = make_uint4(q.x & m.x, q.y & m.y, q.z & m.z, q.w & m.w);
+    }
+    return r;
+  }
+  // ones where the unit's columns exist
+  __device__ static __forceinline__ uint4 mask(int c, int cols) {
+    const int low = c < 0 ? -c * 8 * Elem : 0, high = c + V > cols ? (c + V - cols) * 8 * Elem : 0;  // bits
+    uint64_t a = ~0ull, b = ~0ull;  // low, high half
+    a = low >= 64 ? 0ull : a << low;
+    b = low > 64 ? b << (low - 64) : b;
+    b = high >= 64 ? 0ull : b & (~0ull >> high);
+    a = high > 64 ? a & (~0ull >> (high - 64)) : a;
+    return make_uint4(static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), static_cast<uint32_t>(b),
+                      static_cast<uint32_t>(b >> 32));
   }
   __device__ __forceinline__ void pairs(float2 (&out)[Pairs]) const {
-    if constexpr (V == 1) {
-      float a[1], b[1];
-      values_of<kBF16, kBytes>(w[0], a);
-      values_of<kBF16, kBytes>(w[Parts - 1], b);
-      out[0] = make_float2(a[0], b[0]);
-    } else {
-      float v[V];
-      values_of<kBF16, kBytes>(w[0], v);
+    float v[V];
+    unpack16<kBF16>(q, v);
 #pragma unroll
-      for (int j = 0; j < Pairs; ++j) out[j] = make_float2(v[2 * j], v[2 * j + 1]);
+    for (int j = 0; j < Pairs; ++j) out[j] = make_float2(v[2 * j], v[2 * j + 1]);
+  }
+  __device__ static __forceinline__ void store(uint8_t* row, int c, int cols, const float2 (&p)[Pairs]) {
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < Pairs; ++j) {
+      v[2 * j] = p[j].x;
+      v[2 * j + 1] = p[j].y;
+    }
+    const uint4 r = pack16<kBF16>(v);
+    uint8_t* to = row + static_cast<int64_t>(c) * Elem;
+    if (whole(c, cols)) {
+      *reinterpret_cast<uint4*>(to) = r;
+    } else {
+      const uint4 m = mask(c, cols);
+      store_masked(to, r.x, m.x);
+      store_masked(to + 4, r.y, m.y);
+      store_masked(to + 8, r.z, m.z);
+      store_masked(to + 12, r.w, m.w);
     }
   }
-  __device__ static __forceinline__ void store(uint8_t* row, int c, int tpr, int cols, const float2 (&p)[Pairs]) {
-    if constexpr (V == 1) {
-      store_elem<kBF16>(row, c, p[0].x);
-      if (c + tpr < cols) store_elem<kBF16>(row, c + tpr, p[0].y);
-    } else {
-      float v[V];
+  __device__ static __forceinline__ void store_masked(uint8_t* p, uint32_t v, uint32_t m) {
+    if (m == 0xFFFFFFFFu) *reinterpret_cast<uint32_t*>(p) = v;
+    else if (m == 0x0000FFFFu) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(v);
+    else if (m == 0xFFFF0000u) *reinterpret_cast<uint16_t*>(p + 2) = static_cast<uint16_t>(v >> 16);
+  }
+  // values where there is no column become 0
+  __device__ static __forceinline__ void clip(int c, int cols, float2 (&p)[Pairs]) {
+    if (!whole(c, cols)) {
 #pragma unroll
       for (int j = 0; j < Pairs; ++j) {
-        v[2 * j] = p[j].x;
-        v[2 * j + 1] = p[j].y;
+        if (!has(c, 2 * j, cols)) p[j].x = 0.0f;
+        if (!has(c, 2 * j + 1, cols)) p[j].y = 0.0f;
       }
-      store_words<kBytes>(row + c * Elem, words_of<kBF16, kBytes>(v));
     }
   }
-  __device__ static __forceinline__ void params(const void* v, bool bf16, int c, int tpr, int cols, float none,
+  __device__ static __forceinline__ void params(const void* v, bool bf16, int c, int cols, float none,
                                                 float2 (&out)[Pairs]) {
-    if constexpr (V == 1) {
-      out[0] = make_float2(load_param(v, bf16, c, none), c + tpr < cols ? load_param(v, bf16, c + tpr, none) : 0.0f);
-    } else {
-      float a[V];
+    float a[V];
+    if constexpr (!kShift) {
       load_params(v, bf16, c, none, a);
+    } else {
 #pragma unroll
-      for (int j = 0; j < Pairs; ++j) out[j] = make_float2(a[2 * j], a[2 * j + 1]);
+      for (int j = 0; j < V; ++j) a[j] = has(c, j, cols) ? load_param(v, bf16, c + j, none) : 0.0f;
     }
+#pragma unroll
+    for (int j = 0; j < Pairs; ++j) out[j] = make_float2(a[2 * j], a[2 * j + 1]);
   }
 };
 
-// The row in registers: kNV accesses of kBytes a thread (kCols columns), which
-// also keeps its columns' parameters; the next row is on its way while this
-// one is summed and written.  kWarp: a warp takes a row, else the block does.
-template <bool kBF16, bool kRms, int kBytes, int kCols, bool kWarp>
+template <bool kBF16, bool kRms, bool kShift, int kCols, bool kWarp>
 __global__ void __launch_bounds__(kWarp ? 128 : 1024)
     norm_fwd_row_kernel(const void* __restrict__ x, const void* __restrict__ gamma, const void* __restrict__ beta,
                         bool param_bf16, int64_t rows, int64_t cols, float eps, void* __restrict__ y,
                         float* __restrict__ mean, float* __restrict__ rstd, int32_t* __restrict__ dev_status) {
-  using U = Units<kBF16, kBytes>;
-  constexpr int kN = kCols / U::Span, kPairs = U::Pairs;
+  using U = Unit<kBF16, kShift>;
+  constexpr int kN = kCols / U::V, kPairs = U::Pairs;
   __shared__ __align__(16) float red[2][32];
   if (!kWarp && threadIdx.x < 64) red[threadIdx.x >> 5][threadIdx.x & 31] = 0.0f;
   if (!kWarp) __syncthreads();
@@ -186,35 +227,37 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
   const int64_t first = kWarp ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
   const int64_t step = kWarp ? static_cast<int64_t>(gridDim.x) * (blockDim.x / 32) : gridDim.x;
   const int64_t rb = cols * U::Elem;
+  const int shift = kShift ? static_cast<int>(first * cols % U::V) : 0;  // step * cols is a multiple of V
   uint32_t turn = 0;
 
+  const uint8_t* x_end = static_cast<const uint8_t*>(x) + rows * rb;
   U w[kN], next[kN];
   auto fetch = [&](int64_t row) {
     const uint8_t* xr = static_cast<const uint8_t*>(x) + row * rb;
 #pragma unroll
     for (int k = 0; k < kN; ++k)
-      if (U::column(t, k, tpr) < ncols) next[k].load(xr, U::column(t, k, tpr), tpr, ncols);
+      if (U::column(t + k * tpr, shift) < ncols) next[k].load(xr, U::column(t + k * tpr, shift), x_end);
   };
   if (first < rows) fetch(first);
   float2 ga[kN][kPairs], be[kRms ? 1 : kN][kPairs];
 #pragma unroll
   for (int k = 0; k < kN; ++k) {
-    const int c = U::column(t, k, tpr);
+    const int c = U::column(t + k * tpr, shift);
     if (c < ncols) {
-      U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, ga[k]);
-      if constexpr (!kRms) U::params(beta, param_bf16, c, tpr, ncols, 0.0f, be[k]);
+      U::params(gamma, param_bf16, c, ncols, 1.0f, ga[k]);
+      if constexpr (!kRms) U::params(beta, param_bf16, c, ncols, 0.0f, be[k]);
     }
   }
   for (int64_t row = first; row < rows; row += step) {
 #pragma unroll
-    for (int k = 0; k < kN; ++k) w[k] = next[k];
+    for (int k = 0; k < kN; ++k) w[k] = next[k].trimmed(U::column(t + k * tpr, shift), ncols);
     if (row + step < rows) fetch(row + step);
     float mu = 0.0f;
     if constexpr (!kRms) {
       float2 s = both(0.0f);
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
-        if (U::column(t, k, tpr) < ncols) {
+        if (U::column(t + k * tpr, shift) < ncols) {
           float2 v[kPairs];
           w[k].pairs(v);
 #pragma unroll
@@ -226,17 +269,16 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
     float2 q = both(0.0f);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int c = U::column(t, k, tpr);
+      const int c = U::column(t + k * tpr, shift);
       if (c < ncols) {
         float2 v[kPairs];
         w[k].pairs(v);
 #pragma unroll
-        for (int j = 0; j < kPairs; ++j) {
+        for (int j = 0; j < kPairs; ++j)
           if constexpr (!kRms) v[j] = add2(v[j], both(-mu));
-          if constexpr (!kRms && U::V == 1)
-            if (c + tpr >= ncols) v[j].y = 0.0f;  // no column there
-          q = fma2(v[j], v[j], q);
-        }
+        if constexpr (!kRms) U::clip(c, ncols, v);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) q = fma2(v[j], v[j], q);
       }
     }
     const float rs = 1.0f / sqrtf(row_sum<kWarp>(q.x + q.y, red, turn) * inv + eps);
@@ -249,7 +291,7 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
     uint8_t* yr = static_cast<uint8_t*>(y) + row * rb;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int c = U::column(t, k, tpr);
+      const int c = U::column(t + k * tpr, shift);
       if (c < ncols) {
         float2 v[kPairs];
         w[k].pairs(v);
@@ -260,7 +302,7 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
           if constexpr (kRms) v[j] = mul2(v[j], ga[k][j]);
           else v[j] = fma2(v[j], ga[k][j], be[k][j]);
         }
-        U::store(yr, c, tpr, ncols, v);
+        U::store(yr, c, ncols, v);
       }
     }
   }
@@ -329,14 +371,14 @@ __device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
   return v;
 }
 
-template <bool kBF16, bool kRms, int kBytes, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
+template <bool kBF16, bool kRms, bool kShift, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     norm_bwd_row_kernel(const void* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ gamma,
                         bool param_bf16, const float* __restrict__ mean, const float* __restrict__ rstd,
                         const void* __restrict__ dres, int64_t rows, int64_t cols, void* __restrict__ dx,
                         float* __restrict__ part_g, float* __restrict__ part_b, int group_threads) {
-  using U = Units<kBF16, kBytes>;
-  constexpr int kN = kCols / U::Span, kPairs = U::Pairs;
+  using U = Unit<kBF16, kShift>;
+  constexpr int kN = kCols / U::V, kPairs = U::Pairs;
   constexpr bool kKeep = kAhead;  // gamma in registers
   constexpr bool kJoin = kMode != 0;
   // [call][sum][group][warp]: a block's 32 warps, or 16 of each group, zeros past the last
@@ -361,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   const int64_t rb = cols * U::Elem;
   int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
   int64_t at = row * rb;
+  const int shift = kShift ? static_cast<int>(row * cols % U::V) : 0;  // step * cols is a multiple of V
   uint32_t turn = 0;
 
   U wx[kN], wd[kN], nx[kN], nd[kN];
@@ -368,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   auto fetch = [&](int64_t r, int64_t from) {
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int c = U::column(t, k, tpr);
+      const int c = U::column(t + k * tpr, shift);
       if (c < ncols) {
-        nx[k].load(static_cast<const uint8_t*>(x) + from, c, tpr, ncols);
-        nd[k].load(static_cast<const uint8_t*>(dy) + from, c, tpr, ncols);
+        nx[k].load(static_cast<const uint8_t*>(x) + from, c, static_cast<const uint8_t*>(x) + rows * rb);
+        nd[k].load(static_cast<const uint8_t*>(dy) + from, c, static_cast<const uint8_t*>(dy) + rows * rb);
       }
     }
     if constexpr (!kRms) nmu = mean[r];
@@ -387,16 +430,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       ag[k][j] = both(0.0f);
       if constexpr (!kRms) ab[k][j] = both(0.0f);
     }
-    const int c = U::column(t, k, tpr);
+    const int c = U::column(t + k * tpr, shift);
     if constexpr (kKeep)
-      if (c < ncols) U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, ga[k]);
+      if (c < ncols) U::params(gamma, param_bf16, c, ncols, 1.0f, ga[k]);
   }
   for (; row < rows; row += step, at += step * rb) {
     const float mu = nmu, rs = nrs;
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      wx[k] = nx[k];
-      wd[k] = nd[k];
+      wx[k] = nx[k].trimmed(U::column(t + k * tpr, shift), ncols);
+      wd[k] = nd[k].trimmed(U::column(t + k * tpr, shift), ncols);
     }
     if constexpr (kAhead)
       if (row + step < rows) fetch(row + step, at + step * rb);
@@ -409,12 +452,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     float2 s1 = both(0.0f), s2 = both(0.0f);
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int c = U::column(t, k, tpr);
+      const int c = U::column(t + k * tpr, shift);
       if (c < ncols) {
         float2 xv[kPairs], dv[kPairs], g[kPairs];
         wx[k].pairs(xv);
         wd[k].pairs(dv);
-        if constexpr (!kKeep) U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, g);
+        if constexpr (!kKeep) U::params(gamma, param_bf16, c, ncols, 1.0f, g);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           if constexpr (kKeep) g[j] = ga[k][j];
@@ -434,8 +477,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (dres) {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-          if (U::column(t, k, tpr) < ncols)
-            wr[k].load(static_cast<const uint8_t*>(dres) + at, U::column(t, k, tpr), tpr, ncols);
+          if (U::column(t + k * tpr, shift) < ncols)
+            wr[k].load(static_cast<const uint8_t*>(dres) + at, U::column(t + k * tpr, shift),
+                       static_cast<const uint8_t*>(dres) + rows * rb);
       }
       float c1 = 0.0f, c2;
       if constexpr (kRms) {
@@ -465,12 +509,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       const float a = -c2 * inv * rs * rs, b = -c1 * inv * rs;
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
-        const int c = U::column(t, k, tpr);
+        const int c = U::column(t + k * tpr, shift);
         if (c < ncols) {
           float2 xv[kPairs], dv[kPairs], g[kPairs];
           wx[k].pairs(xv);
           wd[k].pairs(dv);
-          if constexpr (!kKeep) U::params(gamma, param_bf16, c, tpr, ncols, 1.0f, g);
+          if constexpr (!kKeep) U::params(gamma, param_bf16, c, ncols, 1.0f, g);
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) {
             if constexpr (kKeep) g[j] = ga[k][j];
@@ -484,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
             for (int j = 0; j < kPairs; ++j) dv[j] = add2(dv[j], xv[j]);
           }
-          U::store(static_cast<uint8_t*>(dx) + at, c, tpr, ncols, dv);
+          U::store(static_cast<uint8_t*>(dx) + at, c, ncols, dv);
         }
       }
     }
@@ -498,13 +542,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     if (kJoin) __syncthreads();                                        // the sum before this one is read
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      const int c = U::column(t, k, tpr);
+      const int c = U::column(t + k * tpr, shift);
       if (c < ncols) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          into[c + 2 * j] = acc[k][j].x;
-          if constexpr (U::V > 1) into[c + 2 * j + 1] = acc[k][j].y;
-          else if (c + tpr < ncols) into[c + tpr] = acc[k][j].y;
+          if (U::has(c, 2 * j, ncols)) into[c + 2 * j] = acc[k][j].x;
+          if (U::has(c, 2 * j + 1, ncols)) into[c + 2 * j + 1] = acc[k][j].y;
         }
       }
     }
@@ -554,31 +597,48 @@ cudaError_t resident_blocks(Kernel kernel, int threads, int (&cache)[33], int* b
   return cudaSuccess;
 }
 
-template <bool kBF16, bool kRms, int kBytes, int kCols, bool kWarp>
+// Threads that hold `cols` columns, kCols each, at any shift.
+template <bool kBF16, bool kShift>
+int row_threads(int64_t cols, int per_thread) {
+  const int64_t held = cols + (kShift ? kVec<kBF16> - 1 : 0);
+  return static_cast<int>((held + 32 * per_thread - 1) / (32 * per_thread) * 32);
+}
+
+// Blocks, such that the rows of a group are a multiple of V apart where it
+// takes more than one (kShift): as many as fit at once.
+template <bool kBF16, bool kShift>
+int64_t row_blocks(int64_t rows, int64_t groups, int64_t resident) {
+  const int64_t blocks = (rows + groups - 1) / groups;
+  if (blocks <= resident) return blocks;
+  return kShift ? std::max<int64_t>(resident / kVec<kBF16> * kVec<kBF16>, kVec<kBF16>) : resident;
+}
+
+template <bool kBF16, bool kRms, bool kShift, int kCols, bool kWarp>
 cudaError_t norm_fwd_row(const DeviceInfo* di, const FwdArgs& a, int threads) {
-  auto kernel = norm_fwd_row_kernel<kBF16, kRms, kBytes, kCols, kWarp>;
+  auto kernel = norm_fwd_row_kernel<kBF16, kRms, kShift, kCols, kWarp>;
   static int cache[33] = {};
   int per_sm = 1;
   cudaError_t e = resident_blocks(kernel, threads, cache, &per_sm);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = kWarp ? (a.rows + 3) / 4 : a.rows, most = static_cast<int64_t>(di->sm_count) * per_sm;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(threads), 0, a.stream, 1u,
-                    a.x, a.gamma, a.beta, a.param_bf16, a.rows, a.cols, a.eps, a.y, a.mean, a.rstd, a.dev_status);
+  const int64_t blocks =
+      row_blocks<kBF16, kShift>(a.rows, kWarp ? 4 : 1, static_cast<int64_t>(di->sm_count) * per_sm);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, a.stream, 1u, a.x, a.gamma, a.beta,
+                    a.param_bf16, a.rows, a.cols, a.eps, a.y, a.mean, a.rstd, a.dev_status);
 }
 
-template <bool kBF16, bool kRms, int kBytes>
-cudaError_t norm_fwd_bytes(const DeviceInfo* di, const FwdArgs& a, bool* taken) {
+template <bool kBF16, bool kRms, bool kShift>
+cudaError_t norm_fwd_rows(const DeviceInfo* di, const FwdArgs& a, bool* taken) {
+  constexpr int kSlack = kShift ? kVec<kBF16> - 1 : 0;
   *taken = true;
-  if (a.cols <= 256) return norm_fwd_row<kBF16, kRms, kBytes, 8, true>(di, a, 128);
-  if (a.cols <= 512) return norm_fwd_row<kBF16, kRms, kBytes, 16, true>(di, a, 128);
-  // 16 columns a thread where they and their parameters fit 64 registers (bf16
-  // in whole vectors), else 8: 4096 x 4096 bf16 layer 15.5 against 20.3 us, but
-  // float32 32.1 against 24.1, and 8192 x 1537 bf16 56.7 against 27.2.
-  constexpr bool kWide = kBF16 && (kBytes == 16 || (kRms && kBytes == 4));
-  auto threads = [&](int c) { return static_cast<int>((a.cols + 32 * c - 1) / (32 * c) * 32); };
-  if constexpr (!kWide)
-    if (a.cols <= 8192) return norm_fwd_row<kBF16, kRms, kBytes, 8, false>(di, a, threads(8));
-  if (a.cols <= 16384) return norm_fwd_row<kBF16, kRms, kBytes, 16, false>(di, a, threads(16));
+  if (a.cols + kSlack <= 256) return norm_fwd_row<kBF16, kRms, kShift, 8, true>(di, a, 128);
+  if (a.cols + kSlack <= 512) return norm_fwd_row<kBF16, kRms, kShift, 16, true>(di, a, 128);
+  // 16 columns a thread where they and their parameters fit 64 registers
+  // (bf16), else 8: 4096 x 4096 bf16 layer 15.5 against 20.3 us, but float32
+  // 32.1 against 24.1.
+  auto threads = [&](int c) { return row_threads<kBF16, kShift>(a.cols, c); };
+  if constexpr (!kBF16)
+    if (threads(8) <= 1024) return norm_fwd_row<kBF16, kRms, kShift, 8, false>(di, a, threads(8));
+  if (threads(16) <= 1024) return norm_fwd_row<kBF16, kRms, kShift, 16, false>(di, a, threads(16));
   *taken = false;
   return cudaSuccess;
 }
@@ -588,10 +648,8 @@ cudaError_t norm_fwd_t(const FwdArgs& a) {
   const DeviceInfo* di = current_device_info();
   if (!di) return cudaErrorInvalidDevice;
   bool taken = false;
-  const int64_t bytes = a.cols * (kBF16 ? 2 : 4);  // every row begins on a multiple of what divides this
-  cudaError_t e = bytes % 16 == 0  ? norm_fwd_bytes<kBF16, kRms, 16>(di, a, &taken)
-                  : bytes % 4 == 0 ? norm_fwd_bytes<kBF16, kRms, 4>(di, a, &taken)
-                                   : norm_fwd_bytes<kBF16, kRms, kBF16 ? 2 : 4>(di, a, &taken);
+  cudaError_t e = a.cols % kVec<kBF16> == 0 ? norm_fwd_rows<kBF16, kRms, false>(di, a, &taken)
+                                            : norm_fwd_rows<kBF16, kRms, true>(di, a, &taken);
   if (e != cudaSuccess || taken) return e;
   const unsigned grid = static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20));
   return launch_pdl(norm_fwd_kernel<kBF16, kRms>, dim3(grid), dim3(kRowThreads), 0, a.stream, 1u, a.x, a.gamma, a.beta,
@@ -619,10 +677,10 @@ void norm_bwd_outputs(BwdArgs& a, int parts) {
   }
 }
 
-template <bool kBF16, bool kRms, int kBytes, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
+template <bool kBF16, bool kRms, bool kShift, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
 cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
-  auto kernel = norm_bwd_row_kernel<kBF16, kRms, kBytes, kCols, kMode, kThreads, kBlocks, kAhead>;
-  const int tpr = kMode == 2 ? 32 : static_cast<int>((a.cols + 32 * kCols - 1) / (32 * kCols) * 32);
+  auto kernel = norm_bwd_row_kernel<kBF16, kRms, kShift, kCols, kMode, kThreads, kBlocks, kAhead>;
+  const int tpr = kMode == 2 ? 32 : row_threads<kBF16, kShift>(a.cols, kCols);
   int groups = kMode == 0 ? 1 : std::min(kThreads / tpr, kMaxGroups);
   // few rows: one a group
   const int64_t sms = di->sm_count;
@@ -631,29 +689,30 @@ cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
   int per_sm = 1;
   cudaError_t e = resident_blocks(kernel, groups * tpr, cache, &per_sm);
   if (e != cudaSuccess) return e;
-  int64_t blocks = std::min((a.rows + groups - 1) / groups, sms * std::min(per_sm, 3));
-  blocks = std::min<int64_t>(blocks, norm_parts(a.rows));
+  const int64_t blocks = row_blocks<kBF16, kShift>(
+      a.rows, groups, std::min<int64_t>(sms * std::min(per_sm, 3), norm_parts(a.rows)));
   *parts = static_cast<int>(blocks);
   norm_bwd_outputs(a, *parts);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(groups * tpr), 0, a.stream, 1u, a.dy, a.x,
                     a.gamma, a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, tpr);
 }
 
-template <bool kBF16, bool kRms, int kBytes>
-cudaError_t norm_bwd_bytes(const DeviceInfo* di, BwdArgs a, int* parts) {
-  if constexpr (kBF16 && kBytes == 16) {
-    if (a.cols <= 256) return norm_bwd_row<kBF16, kRms, kBytes, 8, 2, 256, 1, true>(di, a, parts);
-    if (a.cols <= 512) return norm_bwd_row<kBF16, kRms, kBytes, 16, 2, 256, 2, true>(di, a, parts);
-    if (a.cols <= 4096) return norm_bwd_row<kBF16, kRms, kBytes, 16, 1, 256, 2, true>(di, a, parts);
-    if (a.cols <= 8192) return norm_bwd_row<kBF16, kRms, kBytes, 16, 0, 512, 1, true>(di, a, parts);
-    if (a.cols <= 16384) return norm_bwd_row<kBF16, kRms, kBytes, 16, 0, 1024, 1, false>(di, a, parts);
+template <bool kBF16, bool kRms, bool kShift>
+cudaError_t norm_bwd_rows(const DeviceInfo* di, BwdArgs a, int* parts) {
+  constexpr int kSlack = kShift ? kVec<kBF16> - 1 : 0;
+  const int64_t held = a.cols + kSlack;
+  if constexpr (kBF16) {
+    if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 256, 1, true>(di, a, parts);
+    if (held <= 512) return norm_bwd_row<kBF16, kRms, kShift, 16, 2, 256, 2, true>(di, a, parts);
+    if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 256, 2, true>(di, a, parts);
+    if (held <= 8192) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 512, 1, true>(di, a, parts);
   } else {
-    if (a.cols <= 256) return norm_bwd_row<kBF16, kRms, kBytes, 8, 2, 512, 1, true>(di, a, parts);
-    if (a.cols <= 2048) return norm_bwd_row<kBF16, kRms, kBytes, 8, 1, 512, 1, true>(di, a, parts);
-    if (a.cols <= 4096) return norm_bwd_row<kBF16, kRms, kBytes, 8, 0, 512, 1, true>(di, a, parts);
-    if (a.cols <= 8192) return norm_bwd_row<kBF16, kRms, kBytes, 8, 0, 1024, 1, true>(di, a, parts);
-    if (a.cols <= 16384) return norm_bwd_row<kBF16, kRms, kBytes, 16, 0, 1024, 1, false>(di, a, parts);
+    if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 512, 1, true>(di, a, parts);
+    if (held <= 2048) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 512, 1, true>(di, a, parts);
+    if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 512, 1, true>(di, a, parts);
+    if (held <= 8192) return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 1024, 1, true>(di, a, parts);
   }
+  if (held <= 16384) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 1024, 1, false>(di, a, parts);
   *parts = norm_parts(a.rows);
   norm_bwd_outputs(a, *parts);
   return launch_pdl(norm_bwd_kernel<kBF16, kRms>, dim3(*parts), dim3(kRowThreads), 0, a.stream, 1u, a.dy, a.x, a.gamma,
@@ -664,10 +723,8 @@ template <bool kBF16, bool kRms>
 cudaError_t norm_bwd_t(const BwdArgs& a, int* parts) {
   const DeviceInfo* di = current_device_info();
   if (!di) return cudaErrorInvalidDevice;
-  const int64_t bytes = a.cols * (kBF16 ? 2 : 4);  // every row begins on a multiple of what divides this
-  return bytes % 16 == 0  ? norm_bwd_bytes<kBF16, kRms, 16>(di, a, parts)
-         : bytes % 4 == 0 ? norm_bwd_bytes<kBF16, kRms, 4>(di, a, parts)
-                          : norm_bwd_bytes<kBF16, kRms, kBF16 ? 2 : 4>(di, a, parts);
+  return a.cols % kVec<kBF16> == 0 ? norm_bwd_rows<kBF16, kRms, false>(di, a, parts)
+                                   : norm_bwd_rows<kBF16, kRms, true>(di, a, parts);
 }
 
 }  // namespace
