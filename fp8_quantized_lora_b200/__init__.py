@@ -539,18 +539,21 @@ def _device_of(t, name, dtypes):
     return t.device
 
 
-def _like(v, t):
-    """An output with the shape and type of `t`: True (allocate), a tensor, or None (not wanted)."""
+def _like(v, name, t, dev):
+    """(tensor, address) of an output with the shape and type of `t`: True
+    (allocate), a tensor, or None (not wanted)."""
     if v is True:
-        return torch.empty_like(t)
-    return None if v is False else v
+        v = torch.empty_like(t)
+        return v, v.data_ptr()
+    return (None, None) if v is None or v is False else (v, _addr(v, name, t.shape, (t.dtype,), dev))
 
 
-def _vector(v, n, t):
-    """The same for `n` float32 on the device of `t`."""
+def _vector(v, name, n, t, dev):
+    """The same for `n` float32 beside `t`."""
     if v is True:
-        return t.new_empty((n,), dtype=torch.float32)
-    return None if v is False else v
+        v = t.new_empty((n,), dtype=torch.float32)
+        return v, v.data_ptr()
+    return (None, None) if v is None or v is False else (v, _addr(v, name, (n,), _F32, dev))
 
 
 def _scratch(op, M, N, K, dev, workspace):
@@ -590,14 +593,14 @@ def falqon_norm_fwd(x, gamma=None, beta=None, eps=1e-5, kind=NORM_LAYER, y=True,
     pdtypes = _EITHER if param is None else (param.dtype,)
     if param is not None and param.dtype not in _DTYPES:
         raise ValueError(f"gamma and beta must be bfloat16 or float32, got {param.dtype}")
-    y = _like(True if y is None else y, x)
-    mean = _vector(None if kind == NORM_RMS and mean is True else mean, rows, x)
-    rstd = _vector(rstd, rows, x)
+    xp = _addr(x, "x", shape, (dtype,), dev)
+    y, yp = _like(True if y is None else y, "y", x, dev)
+    mean, mp = _vector(None if kind == NORM_RMS and mean is True else mean, "mean", rows, x, dev)
+    rstd, rp = _vector(rstd, "rstd", rows, x, dev)
     st = lib().falqon_norm_fwd(
-        _addr(x, "x", shape, (dtype,), dev), _DTYPES[dtype], _addr(gamma, "gamma", (cols,), pdtypes, dev),
+        xp, _DTYPES[dtype], _addr(gamma, "gamma", (cols,), pdtypes, dev),
         _addr(beta, "beta", (cols,), pdtypes, dev), DTYPE_BF16 if param is None else _DTYPES[param.dtype], kind, rows,
-        cols, eps, _addr(y, "y", shape, (dtype,), dev), _addr(mean, "mean", (rows,), _F32, dev),
-        _addr(rstd, "rstd", (rows,), _F32, dev), _status(dev_status, dev), _raw_stream(dev))
+        cols, eps, yp, mp, rp, _status(dev_status, dev), _raw_stream(dev))
     _check(st, "falqon_norm_fwd")
     return y, mean, rstd
 
@@ -616,19 +619,19 @@ def falqon_norm_bwd(dy, x, gamma, mean, rstd, kind=NORM_LAYER, dres=None, dx=Tru
     rows, cols = shape
     dtype = x.dtype
     own = (dtype,)
-    dx = _like(dx, x)
-    dgamma = _vector(dgamma, cols, x)
-    dbeta = _vector(None if kind == NORM_RMS and dbeta is True else dbeta, cols, x)
+    xp = _addr(x, "x", shape, own, dev)
+    dx, dxp = _like(dx, "dx", x, dev)
+    dgamma, dgp = _vector(dgamma, "dgamma", cols, x, dev)
+    dbeta, dbp = _vector(None if kind == NORM_RMS and dbeta is True else dbeta, "dbeta", cols, x, dev)
     ws, wsp, wsb = (None, None, 0)
     if dgamma is not None or dbeta is not None:
         ws, wsp, wsb = _scratch(OP_NORM_BWD, rows, 0, cols, dev, workspace)
     st = lib().falqon_norm_bwd(
-        _addr(dy, "dy", shape, own, dev), _addr(x, "x", shape, own, dev), _DTYPES[dtype],
+        _addr(dy, "dy", shape, own, dev), xp, _DTYPES[dtype],
         _addr(gamma, "gamma", (cols,), _EITHER, dev), DTYPE_BF16 if gamma is None else _DTYPES[gamma.dtype], kind,
         _addr(mean, "mean", (rows,), _F32, dev), _addr(rstd, "rstd", (rows,), _F32, dev),
-        _addr(dres, "dres", shape, own, dev), rows, cols, _addr(dx, "dx", shape, own, dev),
-        _addr(dgamma, "dgamma", (cols,), _F32, dev), _addr(dbeta, "dbeta", (cols,), _F32, dev),
-        _status(dev_status, dev), wsp, wsb, _raw_stream(dev))
+        _addr(dres, "dres", shape, own, dev), rows, cols, dxp, dgp, dbp, _status(dev_status, dev), wsp, wsb,
+        _raw_stream(dev))
     _check(st, "falqon_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -650,12 +653,15 @@ def falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias=None, act=ACT_NONE, residu
     out = (M, N)
     if y is True or y is None:
         y = xq.new_empty(out, dtype=torch.bfloat16)
-    z = _like(z, y)
+        yp = y.data_ptr()
+    else:
+        yp = _addr(y, "y", out, _BF16, dev)
+    z, zp = _like(z, "z", y, dev)
     st = lib().falqon_linear_fwd_epilogue(
         _addr(xq, "xq", (M, K), _CODES, dev), _scalar(s_x, "s_x", dev), _addr(wq, "wq", (N, K), _CODES, dev),
         _scalar(s_w, "s_w", dev), _addr(bias, "bias", (N,), _EITHER, dev),
         DTYPE_BF16 if bias is None else _DTYPES[bias.dtype], act, _addr(residual, "residual", out, _BF16, dev), M, N, K,
-        _addr(z, "z", out, _BF16, dev), _addr(y, "y", out, _BF16, dev), _status(dev_status, dev), _raw_stream(dev))
+        zp, yp, _status(dev_status, dev), _raw_stream(dev))
     _check(st, "falqon_linear_fwd_epilogue")
     return y, z
 
@@ -671,14 +677,14 @@ def falqon_linear_epilogue_bwd(dy, z, act, dz=True, dbias=True, workspace=None, 
             return falqon_linear_epilogue_bwd(dy, z, act, dz, dbias, workspace)
     shape = dy.shape
     M, N = shape
-    dz = _like(dz, dy)
-    dbias = _vector(dbias, N, dy)
+    dyp = _addr(dy, "dy", shape, _BF16, dev)
+    dz, dzp = _like(dz, "dz", dy, dev)
+    dbias, dbp = _vector(dbias, "dbias", N, dy, dev)
     ws, wsp, wsb = (None, None, 0)
     if dbias is not None:
         ws, wsp, wsb = _scratch(OP_LINEAR_EPILOGUE_BWD, M, N, 0, dev, workspace)
     st = lib().falqon_linear_epilogue_bwd(
-        _addr(dy, "dy", shape, _BF16, dev), _addr(z, "z", shape, _BF16, dev), act, M, N,
-        _addr(dz, "dz", shape, _BF16, dev), _addr(dbias, "dbias", (N,), _F32, dev), wsp, wsb, _raw_stream(dev))
+        dyp, _addr(z, "z", shape, _BF16, dev), act, M, N, dzp, dbp, wsp, wsb, _raw_stream(dev))
     _check(st, "falqon_linear_epilogue_bwd")
     return dz, dbias
 
@@ -732,11 +738,11 @@ def falqon_clip_grads(grads, max_norm, factor=1.0, out=None, norm=None, coef=Non
         if len(o) != len(g) or o.device != dev or bytes(o.numel) != bytes(g.numel) or \
                 bytes(o.dtypes) != bytes(g.dtypes):
             raise ValueError("out must match grads in number, sizes, types and device")
-    norm = _vector(True if norm is None else norm, 1, g.tensors[0])
-    coef = _vector(True if coef is None else coef, 1, g.tensors[0])
+    norm, np_ = _vector(True if norm is None else norm, "norm", 1, g.tensors[0], dev)
+    coef, cp = _vector(True if coef is None else coef, "coef", 1, g.tensors[0], dev)
     ws, wsp, wsb = _scratch(OP_CLIP_GRADS, 0, 0, 0, dev, workspace)
     st = lib().falqon_clip_grads(len(g), g.pointers, g.dtypes, g.numel, max_norm, factor,
-                                 None if o is None else o.pointers, _scalar(norm, "norm", dev),
-                                 _scalar(coef, "coef", dev), _status(dev_status, dev), wsp, wsb, _raw_stream(dev))
+                                 None if o is None else o.pointers, np_, cp, _status(dev_status, dev), wsp, wsb,
+                                 _raw_stream(dev))
     _check(st, "falqon_clip_grads")
     return (None if o is None else o.tensors), norm, coef
