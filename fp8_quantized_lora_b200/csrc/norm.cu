@@ -72,6 +72,18 @@ __device__ __forceinline__ float sum_warps(const float* r, int warps) {
   return s;
 }
 
+// The same for a number known when compiled.
+template <int kWarps>
+__device__ __forceinline__ float sum_warps(const float* r) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kWarps; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(r + i);
+    s += (v.x + v.y) + (v.z + v.w);
+  }
+  return s;
+}
+
 // Asks for [p, p + bytes) of a matrix that ends at `end` to come into L2 (whole
 // 16-byte units; one thread).
 __device__ __forceinline__ void prefetch_l2(const uint8_t* p, int64_t bytes, const uint8_t* end) {
@@ -379,7 +391,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
                         float* __restrict__ part_g, float* __restrict__ part_b, int group_threads) {
   using U = Unit<kBF16, kShift>;
   constexpr int kN = kCols / U::V, kPairs = U::Pairs;
-  constexpr bool kKeep = kAhead;  // gamma in registers
+  constexpr bool kKeep = kAhead;           // gamma in registers
+  // and, from the sums to dx, x - mu and g dy rs instead of x and dy: in bf16
+  // that takes 32 registers for 16, which layer norm does not have
+  constexpr bool kHold = kThreads <= 512 && (kRms || !kBF16);
   constexpr bool kJoin = kMode != 0;
   // [call][sum][group][warp]: a block's 32 warps, or 16 of each group, zeros past the last
   constexpr int kRow = kMode == 0 ? 32 : 16 * (kMaxGroups + 1);
@@ -406,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   const int shift = kShift ? static_cast<int>(row * cols % U::V) : 0;  // step * cols is a multiple of V
   uint32_t turn = 0;
 
-  U wx[kN], wd[kN], nx[kN], nd[kN];
+  U wx[kHold ? 1 : kN], wd[kHold ? 1 : kN], nx[kN], nd[kN];
   float nmu = 0.0f, nrs = 0.0f;
   auto fetch = [&](int64_t r, int64_t from) {
 #pragma unroll
@@ -436,10 +451,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   }
   for (; row < rows; row += step, at += step * rb) {
     const float mu = nmu, rs = nrs;
+    float2 xc[kHold ? kN : 1][kPairs], gd[kHold ? kN : 1][kPairs];  // x - mu and g dy rs
 #pragma unroll
     for (int k = 0; k < kN; ++k) {
-      wx[k] = nx[k].trimmed(U::column(t + k * tpr, shift), ncols);
-      wd[k] = nd[k].trimmed(U::column(t + k * tpr, shift), ncols);
+      if constexpr (kHold) {
+        nx[k].trimmed(U::column(t + k * tpr, shift), ncols).pairs(xc[k]);
+        nd[k].trimmed(U::column(t + k * tpr, shift), ncols).pairs(gd[k]);
+      } else {
+        wx[k] = nx[k].trimmed(U::column(t + k * tpr, shift), ncols);
+        wd[k] = nd[k].trimmed(U::column(t + k * tpr, shift), ncols);
+      }
     }
     if constexpr (kAhead)
       if (row + step < rows) fetch(row + step, at + step * rb);
@@ -455,19 +476,32 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       const int c = U::column(t + k * tpr, shift);
       if (c < ncols) {
         float2 xv[kPairs], dv[kPairs], g[kPairs];
-        wx[k].pairs(xv);
-        wd[k].pairs(dv);
+        if constexpr (kHold) {
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            xv[j] = xc[k][j];
+            dv[j] = gd[k][j];
+          }
+        } else {
+          wx[k].pairs(xv);
+          wd[k].pairs(dv);
+        }
         if constexpr (!kKeep) U::params(gamma, param_bf16, c, ncols, 1.0f, g);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           if constexpr (kKeep) g[j] = ga[k][j];
           if constexpr (!kRms) xv[j] = add2(xv[j], both(-mu));
-          const float2 p = mul2(dv[j], mul2(xv[j], both(rs)));
-          ag[k][j] = add2(ag[k][j], p);
-          s2 = fma2(g[j], p, s2);
+          const float2 dr = mul2(dv[j], both(rs));
+          const float2 gr = mul2(g[j], dr);
+          ag[k][j] = fma2(dr, xv[j], ag[k][j]);
+          s2 = fma2(gr, xv[j], s2);
           if constexpr (!kRms) {
             ab[k][j] = add2(ab[k][j], dv[j]);
-            s1 = fma2(g[j], dv[j], s1);
+            s1 = add2(s1, gr);
+          }
+          if constexpr (kHold) {
+            xc[k][j] = xv[j];
+            gd[k][j] = gr;
           }
         }
       }
@@ -502,25 +536,37 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           if (lane == 16) r[kRow + warp] = c2;
         if constexpr (kMode == 0) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-        c2 = sum_warps(r, tpr >> 5);
-        if constexpr (!kRms) c1 = sum_warps(r + kRow, tpr >> 5);
+        constexpr int kWarps = kMode == 1 ? 8 : kThreads / 32;  // a group of several has at most 256 threads
+        c2 = sum_warps<kWarps>(r);
+        if constexpr (!kRms) c1 = sum_warps<kWarps>(r + kRow);
       }
-      // dx = g dy rs + (x - mu) a + b
-      const float a = -c2 * inv * rs * rs, b = -c1 * inv * rs;
+      // with g the sum of g dy rs: dx = g dy rs + (x - mu) a + b
+      const float a = -c2 * inv * rs * rs, b = -c1 * inv;
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const int c = U::column(t + k * tpr, shift);
         if (c < ncols) {
           float2 xv[kPairs], dv[kPairs], g[kPairs];
-          wx[k].pairs(xv);
-          wd[k].pairs(dv);
-          if constexpr (!kKeep) U::params(gamma, param_bf16, c, ncols, 1.0f, g);
+          if constexpr (kHold) {
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+              xv[j] = xc[k][j];
+              dv[j] = gd[k][j];
+            }
+          } else {
+            wx[k].pairs(xv);
+            wd[k].pairs(dv);
+            if constexpr (!kKeep) U::params(gamma, param_bf16, c, ncols, 1.0f, g);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+              if constexpr (kKeep) g[j] = ga[k][j];
+              if constexpr (!kRms) xv[j] = add2(xv[j], both(-mu));
+              dv[j] = mul2(g[j], mul2(dv[j], both(rs)));
+            }
+          }
 #pragma unroll
           for (int j = 0; j < kPairs; ++j) {
-            if constexpr (kKeep) g[j] = ga[k][j];
-            if constexpr (!kRms) xv[j] = add2(xv[j], both(-mu));
-            const float2 gd = mul2(dv[j], g[j]);
-            dv[j] = kRms ? mul2(gd, both(rs)) : fma2(gd, both(rs), both(b));
+            if constexpr (!kRms) dv[j] = add2(dv[j], both(b));
             dv[j] = fma2(xv[j], both(a), dv[j]);
           }
           if (dres) {
