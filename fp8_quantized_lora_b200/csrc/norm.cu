@@ -7,11 +7,27 @@
 //   dx = rstd (g - c1 - xh c2) + dres
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 //
-// Both directions are bound by HBM: 2 (forward) or 3 to 4 (backward) elements
-// of the matrix per element.  The variance is taken about the mean, not as
-// the difference of two moments, so a large common offset costs no digits.
-// Statistics, sums and the parameter gradients are float32; one rounding per
-// output element.
+// The variance is taken about the mean, not as the difference of two moments,
+// so a large common offset costs no digits.  Statistics, sums and the parameter
+// gradients are float32; one rounding per output element.
+//
+// What cannot be done without is HBM traffic: 2 (forward) or 3 to 4 (backward)
+// elements of the matrix per element.  A row stays in registers between its
+// sums and its outputs, so it is read once; the threads that share it meet at
+// one barrier for each sum that the next step waits for.  Measured on a B200
+// (us, floor at 6.55 TB/s in brackets):
+//   forward   4096 x 4096 bf16   RMS 12.9, layer 15.4 (10.2)
+//             4096 x 4096 fp32   RMS 23.2, layer 24.4 (20.5)
+//             8192 x 1537 bf16   RMS 12.8, layer 19.4 (7.7)
+//   backward  8192 x 4096 bf16 + dres   RMS 46.7, layer 56.6 (41.0)
+//             4096 x 4096 bf16   RMS 23.6, layer 30.8 (15.4)
+//             4096 x 4096 fp32   RMS 34.2, layer 36.9 (30.7)
+//             8192 x 1537 bf16   RMS 24.3, layer 34.8 (11.5)
+//              300 x 4096 bf16   RMS 6.0, layer 7.4 (1.1)
+// (the backward with its second kernel, which joins the blocks' sums over the
+// rows: about 2.5 us).  float32 is near its bound; in bf16 the backward's
+// instructions and their latency bound it: a bf16 value costs an instruction
+// to widen, and 128 registers a thread leave 16 warps an SM.
 #include <algorithm>
 
 #include "elem.cuh"
@@ -23,8 +39,8 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// One row per block iteration; three passes over the row (the second and
-// third out of L1 / L2).
+// Rows of more than 16384 columns: one row per block iteration, three passes
+// over it (the second and third out of L1 / L2).
 template <bool kBF16, bool kRms>
 __global__ void __launch_bounds__(kRowThreads)
     norm_fwd_kernel(const void* __restrict__ x, const void* __restrict__ gamma, const void* __restrict__ beta,
@@ -320,14 +336,15 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
   }
 }
 
-// Block b owns the rows [b rows / grid, (b + 1) rows / grid) and one row of
-// each partial sum; a thread owns its columns of them.
+// Rows of more than 16384 columns: block b owns the rows [b rows / grid,
+// (b + 1) rows / grid) and one row of each partial sum, in memory; a thread
+// owns its columns of them.
 template <bool kBF16, bool kRms>
 __global__ void __launch_bounds__(kRowThreads)
     norm_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ gamma,
                     bool param_bf16, const float* __restrict__ mean, const float* __restrict__ rstd,
                     const void* __restrict__ dres, int64_t rows, int64_t cols, void* __restrict__ dx,
-                    float* __restrict__ part_g, float* __restrict__ part_b) {
+                    float* __restrict__ part_g, float* __restrict__ part_b, int32_t* __restrict__ dev_status) {
   pdl_trigger();
   pdl_wait();
   __shared__ float red[32];
@@ -351,6 +368,7 @@ __global__ void __launch_bounds__(kRowThreads)
     if (!dx) continue;
     c1 = kRms ? 0.0f : block_sum(c1, red) * inv;
     c2 = block_sum(c2, red) * inv;
+    if (threadIdx.x == 0 && dev_status && !isfinite((c1 + c2) * rs)) atomicOr(dev_status, kDevNonfinite);
     for (int64_t c = threadIdx.x; c < cols; c += kRowThreads) {
       const float xh = (load_elem<kBF16>(x, base + c) - mu) * rs;
       const float gv = load_elem<kBF16>(dy, base + c) * load_param(gamma, param_bf16, c, 1.0f);
@@ -362,15 +380,22 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // ---------------------------------------------------------------- backward: rows in registers
-// A group of threads takes a row at a time, 8 columns (16 for the longest
-// rows) a thread: their parts of dgamma and dbeta stay in registers over all
-// the rows that the group takes, and the next row of x and dy is on its way
-// while this one is worked on.
+// A group of threads takes a row at a time: its columns' parts of dgamma and
+// dbeta stay in a thread's registers over all the rows that the group takes,
+// and the next row of x and dy is on its way while this one is worked on
+// (kAhead); the row after that is asked for into L2 (float32 39.6 -> 34.3 us).
 //
-// kMode: a block takes a row (0), a group of `tpr` threads (1) or a warp (2);
-// where a block holds several groups it joins their sums at the end.
+// Columns a thread: what a row costs beside its columns (two sums over the
+// group, a barrier, addresses) is paid by every warp of it, so 16 columns
+// instead of 8 take bf16 layer norm from 39 to 32 us at 4096 x 4096, two blocks
+// of 256 threads an SM; float32, whose columns take twice the registers in
+// flight, stays at 8.  The rows streamed through a ring in shared memory by
+// bulk copies instead took 26.6 (RMS) and 36.1 us (layer).
+//
+// kMode: a block takes a row (0), a group of `group_threads` threads (1) or a
+// warp (2); where a block holds several groups it joins their sums at the end.
 constexpr int kMaxGroups = 15;  // a named barrier each beside the block's
-constexpr int kL2Rows = 2;           // rows ahead that are asked for into L2
+constexpr int kL2Rows = 2;      // rows ahead that are asked for into L2
 
 // Two sums over a warp with the shuffles of one: after the first exchange the
 // lower lanes hold the first value's parts and the upper ones the second's.
@@ -388,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     norm_bwd_row_kernel(const void* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ gamma,
                         bool param_bf16, const float* __restrict__ mean, const float* __restrict__ rstd,
                         const void* __restrict__ dres, int64_t rows, int64_t cols, void* __restrict__ dx,
-                        float* __restrict__ part_g, float* __restrict__ part_b, int group_threads) {
+                            float* __restrict__ part_g, float* __restrict__ part_b, int32_t* __restrict__ dev_status,
+                        int group_threads) {
   using U = Unit<kBF16, kShift>;
   constexpr int kN = kCols / U::V, kPairs = U::Pairs;
   constexpr bool kKeep = kAhead;           // gamma in registers
@@ -399,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   // [call][sum][group][warp]: a block's 32 warps, or 16 of each group, zeros past the last
   constexpr int kRow = kMode == 0 ? 32 : 16 * (kMaxGroups + 1);
   __shared__ __align__(16) float red[2][2][kRow];
-  __shared__ float merge[kJoin ? kThreads * kCols : 1];
+  __shared__ __align__(16) float merge[kJoin ? kThreads * kCols : 1];
   if constexpr (kMode != 2) {
     for (int i = static_cast<int>(threadIdx.x); i < 4 * kRow; i += static_cast<int>(blockDim.x))
       (&red[0][0][0])[i] = 0.0f;
@@ -542,6 +568,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       }
       // with g the sum of g dy rs: dx = g dy rs + (x - mu) a + b
       const float a = -c2 * inv * rs * rs, b = -c1 * inv;
+      // a NaN or infinity in the row or its statistics, or sums past float32
+      if (t == 0 && dev_status && !isfinite(a + b)) atomicOr(dev_status, kDevNonfinite);
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const int c = U::column(t + k * tpr, shift);
@@ -592,8 +620,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       if (c < ncols) {
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          if (U::has(c, 2 * j, ncols)) into[c + 2 * j] = acc[k][j].x;
-          if (U::has(c, 2 * j + 1, ncols)) into[c + 2 * j + 1] = acc[k][j].y;
+          if constexpr (kShift) {
+            if (U::has(c, 2 * j, ncols)) into[c + 2 * j] = acc[k][j].x;
+            if (U::has(c, 2 * j + 1, ncols)) into[c + 2 * j + 1] = acc[k][j].y;
+          } else if (j % 2 == 0) {  // whole units begin on 16 bytes of the sums too
+            *reinterpret_cast<float4*>(into + c + 2 * j) =
+                make_float4(acc[k][j].x, acc[k][j].y, acc[k][(j + 1) % kPairs].x, acc[k][(j + 1) % kPairs].y);
+          }
         }
       }
     }
@@ -612,8 +645,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 }
 
 // Blocks of the backward, each with one partial row of dgamma and dbeta: at
-// most one per SM of a B200 (two where the row is too long for the ring),
-// never more than rows.
+// most three per SM of a B200, never more than rows.
 constexpr int64_t kNormParts = 444;
 
 int norm_parts(int64_t rows) { return static_cast<int>(rows < kNormParts ? rows : kNormParts); }
@@ -740,7 +772,7 @@ cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
   *parts = static_cast<int>(blocks);
   norm_bwd_outputs(a, *parts);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(groups * tpr), 0, a.stream, 1u, a.dy, a.x,
-                    a.gamma, a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, tpr);
+                    a.gamma, a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, a.dev_status, tpr);
 }
 
 template <bool kBF16, bool kRms, bool kShift>
@@ -749,6 +781,16 @@ cudaError_t norm_bwd_rows(const DeviceInfo* di, BwdArgs a, int* parts) {
   const int64_t held = a.cols + kSlack;
   if constexpr (kBF16) {
     if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 256, 1, true>(di, a, parts);
+    // few rows: a block each, and half the columns a thread, whose code is
+    // shorter to fetch and run once (layer norms, us: 64 x 4096 10.1 -> 5.8,
+    // 1200 x 4096 17.2 -> 13.2, 1200 x 2048 10.8 -> 8.8, 300 x 1024
+    // 7.9 -> 5.7; it loses where narrow rows are many, 700 x 1024 7.1 -> 7.5,
+    // and on long runs, 8192 x 4096 56.5 -> 58.9).  Rows off their 16 bytes
+    // take it at any count: their masks cost registers that 16 columns do not
+    // leave (8192 x 1537 38.3 -> 34.8; 4096 x 2049 31.4 -> 32.5, RMS 25.5 -> 19.1)
+    if (held <= 4096 && (held <= 1024 ? a.rows <= 3 * di->sm_count
+                                      : kShift || a.rows <= 12 * di->sm_count))
+      return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 512, 1, true>(di, a, parts);
     if (held <= 512) return norm_bwd_row<kBF16, kRms, kShift, 16, 2, 256, 2, true>(di, a, parts);
     if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 256, 2, true>(di, a, parts);
     if (held <= 8192) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 512, 1, true>(di, a, parts);
@@ -762,7 +804,7 @@ cudaError_t norm_bwd_rows(const DeviceInfo* di, BwdArgs a, int* parts) {
   *parts = norm_parts(a.rows);
   norm_bwd_outputs(a, *parts);
   return launch_pdl(norm_bwd_kernel<kBF16, kRms>, dim3(*parts), dim3(kRowThreads), 0, a.stream, 1u, a.dy, a.x, a.gamma,
-                    a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b);
+                    a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, a.dev_status);
 }
 
 template <bool kBF16, bool kRms>

@@ -177,6 +177,27 @@ def test_backward_output_subsets(cuda_device, cols, want):
     _check_bwd(x, None, dy, None, mean, rstd, False, *out)
 
 
+@pytest.mark.parametrize("cols", [40, 333, 4096, 12000, 20000])
+def test_backward_non_finite_row(cuda_device, cols):
+    """An infinity or NaN in a row of dy raises the status bit; the other rows' dx keep their bits."""
+    for rms in (False, True):
+        kind = F.NORM_RMS if rms else F.NORM_LAYER
+        x, gamma, beta, dy, _ = _make(cols, 9, cols, BF, BF, True, rms)
+        _, mean, rstd = F.falqon_norm_fwd(x, gamma, beta, 1e-5, kind)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        good = F.falqon_norm_bwd(dy, x, gamma, mean, rstd, kind, dgamma=None, dbeta=None, dev_status=st)[0]
+        assert int(st.item()) == 0
+        for bad in (math.inf, math.nan):
+            dy2 = dy.clone()
+            dy2[4, cols - 1] = bad
+            st.zero_()
+            dx, dgamma, _ = F.falqon_norm_bwd(dy2, x, gamma, mean, rstd, kind, dev_status=st)
+            assert int(st.item()) == F.DEV_NONFINITE
+            keep = [i for i in range(9) if i != 4]
+            assert torch.equal(dx[keep], good[keep])
+            assert not torch.isfinite(dx[4]).all() and torch.isfinite(dgamma[:cols - 1]).all()
+
+
 def test_gradient_agrees_with_autograd(cuda_device):
     """The whole chain x -> y -> loss against torch's differentiation of the definition in float64."""
     for rms in (False, True):
