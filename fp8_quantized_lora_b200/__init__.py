@@ -502,6 +502,8 @@ def _elsewhere(dev, stream):
     """A scope that makes `dev` and the caller's stream current, or None where
     they are: what is allocated then belongs to the stream that the call runs on."""
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on {dev}")
         return torch.cuda.stream(stream)  # also selects the stream's device
     return None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 

@@ -1,6 +1,7 @@
 // C ABI of libfalqon: argument validation, workspace layout, dispatch.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <memory>
 #include <mutex>
 #include <new>
@@ -539,16 +540,37 @@ falqon_status norm_shape(falqon_dtype dtype, falqon_dtype param_dtype, falqon_no
   return FALQON_OK;
 }
 
+// What a call writes may not overlap what it reads, nor another of its outputs.
+struct Bytes {
+  const void* p;  // null: not given
+  size_t n;
+};
+
+bool overlap(const Bytes& a, const Bytes& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + b.n && y < x + a.n;
+}
+
+bool clobbers(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
+  for (const Bytes* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Bytes& i : ins)
+      if (overlap(*o, i)) return true;
+    for (const Bytes* q = outs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return true;
+  }
+  return false;
+}
+
+size_t bytes_of(falqon_dtype d, int64_t numel) {
+  return static_cast<size_t>(numel) * (d == FALQON_DTYPE_BF16 ? 2 : 4);
+}
+
 // A tensor's bytes in memory, for the overlap checks of falqon_clip_grads.
 struct Span {
   uintptr_t begin, end;
   int index;
   bool operator<(const Span& o) const { return begin < o.begin; }
 };
-
-size_t grad_bytes(falqon_dtype d, int64_t numel) {
-  return static_cast<size_t>(numel) * (d == FALQON_DTYPE_BF16 ? 2 : 4);
-}
 
 // Outputs may not overlap one another, nor any gradient but their own, which
 // they then equal (in place).
@@ -560,14 +582,14 @@ falqon_status clip_overlaps(int n, const void* const* grads, const falqon_dtype*
   for (int i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
     const uintptr_t b = reinterpret_cast<uintptr_t>(outs[i]);
-    span[k++] = Span{b, b + grad_bytes(dtypes[i], numel[i]), i};
+    span[k++] = Span{b, b + bytes_of(dtypes[i], numel[i]), i};
   }
   std::sort(span.get(), span.get() + k);
   for (int i = 1; i < k; ++i)
     if (span[i].begin < span[i - 1].end) return FALQON_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
-    const uintptr_t b = reinterpret_cast<uintptr_t>(grads[i]), e = b + grad_bytes(dtypes[i], numel[i]);
+    const uintptr_t b = reinterpret_cast<uintptr_t>(grads[i]), e = b + bytes_of(dtypes[i], numel[i]);
     // the outputs are disjoint: those that meet [b, e) end with the last one that begins before e
     const Span* s = std::lower_bound(span.get(), span.get() + k, Span{e, 0, 0});
     if (s == span.get()) continue;
@@ -593,6 +615,10 @@ falqon_status falqon_norm_fwd(const void* x, falqon_dtype dtype, const void* gam
   if (unaligned16(x) || unaligned16(y) || unaligned16(gamma) || unaligned16(beta) || unaligned16(mean) ||
       unaligned16(rstd))
     return FALQON_ERR_UNSUPPORTED;
+  const size_t all = bytes_of(dtype, rows * cols), param = bytes_of(param_dtype, cols);
+  const size_t per_row = 4 * static_cast<size_t>(rows);
+  if (clobbers({{y, all}, {mean, per_row}, {rstd, per_row}}, {{x, all}, {gamma, param}, {beta, param}}))
+    return FALQON_ERR_INVALID_ARG;
   if (!current_device_info()) return FALQON_ERR_CUDA;
   return from_cuda(launch_norm_fwd(x, dtype == FALQON_DTYPE_BF16, gamma, beta, param_dtype == FALQON_DTYPE_BF16,
                                    kind == FALQON_NORM_RMS, rows, cols, eps, y, mean, rstd, dev_status,
@@ -616,6 +642,11 @@ falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_dtype dtype,
     s = check_ws(norm_bwd_workspace_bytes(rows, cols), workspace, workspace_bytes);
     if (s != FALQON_OK) return s;
   }
+  const size_t all = bytes_of(dtype, rows * cols), param = bytes_of(param_dtype, cols);
+  const size_t per_row = 4 * static_cast<size_t>(rows), per_col = 4 * static_cast<size_t>(cols);
+  if (clobbers({{dx, all}, {dgamma, per_col}, {dbeta, per_col}},
+               {{dy, all}, {x, all}, {gamma, param}, {mean, per_row}, {rstd, per_row}, {dres, all}}))
+    return FALQON_ERR_INVALID_ARG;
   if (!current_device_info()) return FALQON_ERR_CUDA;
   return from_cuda(launch_norm_bwd(dy, x, dtype == FALQON_DTYPE_BF16, gamma, param_dtype == FALQON_DTYPE_BF16,
                                    kind == FALQON_NORM_RMS, mean, rstd, dres, rows, cols, dx, dgamma, dbeta,
@@ -633,6 +664,10 @@ falqon_status falqon_linear_fwd_epilogue(const uint8_t* xq, const float* s_x, co
   if (unaligned16(xq) || unaligned16(wq) || unaligned16(y) || unaligned16(bias) || unaligned16(residual) ||
       unaligned16(z))
     return FALQON_ERR_UNSUPPORTED;
+  const size_t out = bytes_of(FALQON_DTYPE_BF16, M * N);
+  if (clobbers({{y, out}, {z, out}}, {{xq, static_cast<size_t>(M * K)}, {wq, static_cast<size_t>(N * K)},
+                                      {bias, bytes_of(bias_dtype, N)}, {residual, out}, {s_x, 4}, {s_w, 4}}))
+    return FALQON_ERR_INVALID_ARG;
   if (!current_device_info()) return FALQON_ERR_CUDA;
   const LinearEpilogue epi{bias, bias_dtype == FALQON_DTYPE_BF16, act, residual, z};
   return from_cuda(launch_fp8_gemm_fwd_epilogue(xq, s_x, wq, s_w, M, N, K, epi, y, dev_status,
@@ -651,6 +686,8 @@ falqon_status falqon_linear_epilogue_bwd(const void* dy, const void* z, falqon_a
     falqon_status s = check_ws(epilogue_bwd_workspace_bytes(M, N), workspace, workspace_bytes);
     if (s != FALQON_OK) return s;
   }
+  const size_t all = bytes_of(FALQON_DTYPE_BF16, M * N);
+  if (clobbers({{dz, all}, {dbias, 4 * static_cast<size_t>(N)}}, {{dy, all}, {z, all}})) return FALQON_ERR_INVALID_ARG;
   if (!current_device_info()) return FALQON_ERR_CUDA;
   return from_cuda(launch_epilogue_bwd(dy, z, act, M, N, dz, dbias, workspace, static_cast<cudaStream_t>(stream)));
 }

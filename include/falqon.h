@@ -32,7 +32,9 @@
  *    when that size is 0.  Calls that overlap on the GPU must not share a
  *    workspace.  No other aliasing between arguments is allowed except the
  *    documented in-place operands of falqon_proxy_update and
- *    falqon_clip_grads.
+ *    falqon_clip_grads.  The calls around the linear layer
+ *    (falqon_norm_fwd to falqon_clip_grads) refuse outputs that overlap an
+ *    input or one another with FALQON_ERR_INVALID_ARG.
  *  - A workspace given to falqon_quantize or falqon_quantize_e5m2 must be
  *    initialised once, before its first use, by falqon_workspace_init (or
  *    filled with zero bytes by the caller).  Every quantize call leaves it
@@ -609,7 +611,7 @@ FALQON_API falqon_status falqon_norm_bwd(const void* dy, const void* x, falqon_d
  * falqon_linear_fwd's in the last bit.
  *
  *  xq, s_x, wq, s_w as falqon_linear_fwd.  bias [N] in bias_dtype, nullable.
- *  residual [M, N] bfloat16, nullable; it may not be y or z.
+ *  residual [M, N] bfloat16, nullable.
  *  z [M, N] bfloat16, nullable; y [M, N] bfloat16.
  *  Requirements: as falqon_linear_fwd.
  */

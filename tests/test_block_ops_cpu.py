@@ -86,6 +86,43 @@ def test_linear_epilogue_argument_errors():
     assert bwd(ws=None, wsb=0) == 3 and bwd(wsb=64) == 3 and bwd(ws=P8) == 3
 
 
+def test_outputs_over_inputs_or_one_another_are_refused():
+    def at(i):
+        return C.c_void_p((1 << 20) + (i << 12))
+
+    def refused(f, args, outs, ins):
+        # each output moved onto each input and each other output, and onto its last bytes
+        for o, size in outs.items():
+            for other, n in {**ins, **outs}.items():
+                if other == o:
+                    continue
+                for where in (0, (n - 1) // 16 * 16):
+                    moved = dict(args, **{o: C.c_void_p(args[other].value + where)})
+                    assert f(**moved) == 1, (o, other, where)
+
+    ws, wsb = C.c_void_p(1 << 28), 1 << 24
+    L = F.lib()
+    rows, cols = 8, 24
+    mat, par, per_row, per_col = rows * cols * 2, cols * 2, rows * 4, cols * 4
+    args = {k: at(i) for i, k in enumerate(("x", "gamma", "beta", "y", "mean", "rstd"))}
+    refused(lambda x, gamma, beta, y, mean, rstd: L.falqon_norm_fwd(
+        x, BF, gamma, beta, BF, LAYER, rows, cols, 1e-5, y, mean, rstd, None, None),
+        args, dict(y=mat, mean=per_row, rstd=per_row), dict(x=mat, gamma=par, beta=par))
+    args = {k: at(i) for i, k in enumerate(("dy", "x", "gamma", "mean", "rstd", "dres", "dx", "dg", "db"))}
+    refused(lambda dy, x, gamma, mean, rstd, dres, dx, dg, db: L.falqon_norm_bwd(
+        dy, x, BF, gamma, BF, LAYER, mean, rstd, dres, rows, cols, dx, dg, db, None, ws, wsb, None),
+        args, dict(dx=mat, dg=per_col, db=per_col),
+        dict(dy=mat, x=mat, gamma=par, mean=per_row, rstd=per_row, dres=mat))
+    M, N, K = 4, 32, 48
+    args = {k: at(i) for i, k in enumerate(("xq", "sx", "wq", "sw", "bias", "res", "z", "y"))}
+    refused(lambda xq, sx, wq, sw, bias, res, z, y: L.falqon_linear_fwd_epilogue(
+        xq, sx, wq, sw, bias, BF, 1, res, M, N, K, z, y, None, None),
+        args, dict(z=M * N * 2, y=M * N * 2), dict(xq=M * K, wq=N * K, bias=N * 2, res=M * N * 2, sx=4, sw=4))
+    args = {k: at(i) for i, k in enumerate(("dy", "z", "dz", "db"))}
+    refused(lambda dy, z, dz, db: L.falqon_linear_epilogue_bwd(dy, z, 4, M, N, dz, db, ws, wsb, None),
+            args, dict(dz=M * N * 2, db=N * 4), dict(dy=M * N * 2, z=M * N * 2))
+
+
 def _clip(ptrs=(1 << 20, 1 << 21), dtypes=(BF, F32), numel=(100, 50), max_norm=1.0, factor=1.0, outs=None, norm=P,
           ws=P, wsb=1 << 20, n=None):
     k = len(ptrs)

@@ -8,6 +8,11 @@ the quantized linear layers, as a fine-tuning step of an MLP block uses them:
 Every step is held to its definition on the inputs that it got."""
 
 import math
+import pathlib
+import subprocess
+import sys
+import threading
+import types
 
 import pytest
 import torch
@@ -239,3 +244,108 @@ def test_outputs_aligned_to_16_bytes_only(cuda_device, M, N, K):
     assert all(torch.equal(a, b) for a, b in zip(n, n2))
     c, c2 = F.falqon_clip_grads([res, bias], 1.0, out=True), F.falqon_clip_grads([off(res), off(bias)], 1.0, out=True)
     assert torch.equal(c[0][0], c2[0][0]) and torch.equal(c[1], c2[1])
+
+
+def test_tensors_side_by_side(cuda_device):
+    """Every tensor of a call in one allocation, end to end: apart for the
+    overlap checks, and nothing is written past an output's last element."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows, cols = 40, 1000  # 2 000-byte rows; 160-byte statistics
+    x, dy, dres = (torch.randn(rows, cols, generator=g, device="cuda").to(BF) for _ in range(3))
+    gamma = torch.randn(cols, generator=g, device="cuda").to(BF)
+    mean, rstd = F.falqon_norm_fwd(x, gamma)[1:]
+    want = F.falqon_norm_bwd(dy, x, gamma, mean, rstd, dres=dres)
+    parts = [dy, x, dres, gamma, mean, rstd, *want]
+    sizes = [t.numel() * t.element_size() for t in parts]
+    assert all(s % 16 == 0 for s in sizes)
+    buf = torch.full((sum(sizes) + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    views, at = [], 0
+    for t, s in zip(parts, sizes):
+        views.append(buf[at:at + s].view(t.dtype).view(t.shape))
+        at += s
+    for v, t in zip(views[:6], parts):
+        v.copy_(t)
+    F.falqon_norm_bwd(views[0], views[1], views[3], views[4], views[5], dres=views[2], dx=views[6], dgamma=views[7],
+                      dbeta=views[8])
+    for v, t in zip(views, parts):
+        assert torch.equal(v, t)
+    assert bool((buf[at:] == 0x5A).all())
+
+
+def test_a_stream_of_another_device_is_refused(cuda_device):
+    x = torch.ones(16, 16, device="cuda", dtype=BF)
+    other = types.SimpleNamespace(device=torch.device("cuda", x.device.index + 1))
+    v = torch.ones(16, device="cuda")
+    codes = x.to(torch.float8_e4m3fn)
+    for call in (lambda: F.falqon_norm_fwd(x, stream=other), lambda: F.falqon_norm_bwd(x, x, None, v, v, stream=other),
+                 lambda: F.falqon_linear_fwd_epilogue(codes, v[:1], codes, v[:1], stream=other),
+                 lambda: F.falqon_linear_epilogue_bwd(x, x, F.ACT_RELU, stream=other),
+                 lambda: F.falqon_clip_grads([x], 1.0, stream=other)):
+        with pytest.raises(ValueError):
+            call()
+
+
+def test_calls_from_several_threads(cuda_device):
+    """Threads of one process, each with a stream of its own, from their first call on."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    xs = [torch.randn(300 + 77 * i, 1040, generator=g, device="cuda").to(BF) for i in range(4)]
+    w = (torch.randn(528, 1040, generator=g, device="cuda") / 32).to(torch.float8_e4m3fn)
+    one = torch.ones(1, device="cuda")
+    gamma = torch.randn(1040, generator=g, device="cuda")
+
+    def calls(x):
+        y, mean, rstd = F.falqon_norm_fwd(x, gamma)
+        z = F.falqon_linear_fwd_epilogue(y.to(torch.float8_e4m3fn), one, w, one, act=F.ACT_GELU_ERF, z=True)
+        b = F.falqon_linear_epilogue_bwd(z[0], z[1], F.ACT_GELU_ERF)
+        n = F.falqon_norm_bwd(y, x, gamma, mean, rstd)
+        c, norm, _ = F.falqon_clip_grads([n[0], b[1]], 1.0, out=True)
+        return [y, *z, *b, *n, *c, norm]
+
+    got = [None] * len(xs)
+    torch.cuda.synchronize()
+
+    def run(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                got[i] = calls(xs[i])
+        s.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i, x in enumerate(xs):
+        for a, b in zip(got[i], calls(x), strict=True):
+            assert torch.equal(a, b)
+
+
+FIRST_CALL_CAPTURED = """
+import torch
+import fp8_quantized_lora_b200 as F
+x = torch.randn(300, 1040, device="cuda").to(torch.bfloat16)
+w = (torch.randn(528, 1040, device="cuda") / 32).to(torch.float8_e4m3fn)
+xq = x.to(torch.float8_e4m3fn)
+one, gamma = torch.ones(1, device="cuda"), torch.randn(1040, device="cuda")
+def calls():
+    y, mean, rstd = F.falqon_norm_fwd(x, gamma)
+    o, z = F.falqon_linear_fwd_epilogue(xq, one, w, one, act=F.ACT_SILU, z=True)
+    dz, db = F.falqon_linear_epilogue_bwd(o, z, F.ACT_SILU)
+    n = F.falqon_norm_bwd(y, x, gamma, mean, rstd)
+    c, norm, coef = F.falqon_clip_grads([n[0], db], 1.0, out=True)
+    return [y, mean, rstd, o, z, dz, db, *n, *c, norm, coef]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, calls(), strict=True))
+print("same")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture(cuda_device):
+    p = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], capture_output=True, text=True, timeout=300,
+                       cwd=pathlib.Path(F.__file__).resolve().parents[1])
+    assert p.returncode == 0 and p.stdout.strip() == "same", p.stderr[-2000:]
