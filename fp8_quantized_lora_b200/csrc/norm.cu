@@ -19,11 +19,11 @@
 //   forward   4096 x 4096 bf16   RMS 12.9, layer 15.4 (10.2)
 //             4096 x 4096 fp32   RMS 23.2, layer 24.4 (20.5)
 //             8192 x 1537 bf16   RMS 12.8, layer 19.4 (7.7)
-//   backward  8192 x 4096 bf16 + dres   RMS 46.7, layer 56.6 (41.0)
-//             4096 x 4096 bf16   RMS 23.6, layer 30.8 (15.4)
+//   backward  8192 x 4096 bf16 + dres   RMS 44.9, layer 47.8 (41.0)
+//             4096 x 4096 bf16   RMS 21.4, layer 25.2 (15.4)
 //             4096 x 4096 fp32   RMS 34.2, layer 36.9 (30.7)
-//             8192 x 1537 bf16   RMS 24.3, layer 34.8 (11.5)
-//              300 x 4096 bf16   RMS 6.0, layer 7.4 (1.1)
+//             8192 x 1537 bf16   RMS 24.4, layer 33.6 (11.5)
+//              300 x 4096 bf16   RMS 6.0, layer 7.3 (1.1)
 // (the backward with its second kernel, which joins the blocks' sums over the
 // rows: about 2.5 us).  float32 is near its bound; in bf16 the backward's
 // instructions and their latency bound it: a bf16 value costs an instruction
@@ -387,8 +387,8 @@ __global__ void __launch_bounds__(kRowThreads)
 //
 // Columns a thread: what a row costs beside its columns (two sums over the
 // group, a barrier, addresses) is paid by every warp of it, so 16 columns
-// instead of 8 take bf16 layer norm from 39 to 32 us at 4096 x 4096, two blocks
-// of 256 threads an SM; float32, whose columns take twice the registers in
+// instead of 8 take bf16 layer norm from 29.9 to 25.2 us at 4096 x 4096, two
+// blocks of 256 threads an SM; float32, whose columns take twice the registers in
 // flight, stays at 8.  The rows streamed through a ring in shared memory by
 // bulk copies instead took 26.6 (RMS) and 36.1 us (layer).
 //
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   constexpr int kN = kCols / U::V, kPairs = U::Pairs;
   constexpr bool kKeep = kAhead;           // gamma in registers
   // and, from the sums to dx, x - mu and g dy rs instead of x and dy: in bf16
-  // that takes 32 registers for 16, which layer norm does not have
-  constexpr bool kHold = kThreads <= 512 && (kRms || !kBF16);
+  // that takes 32 registers for 16 (16 columns), which layer norm does not have
+  constexpr bool kHold = kThreads <= 512 && (kRms || !kBF16 || (kMode == 0 && kCols == 8));
   constexpr bool kJoin = kMode != 0;
   // [call][sum][group][warp]: a block's 32 warps, or 16 of each group, zeros past the last
   constexpr int kRow = kMode == 0 ? 32 : 16 * (kMaxGroups + 1);
@@ -782,17 +782,20 @@ cudaError_t norm_bwd_rows(const DeviceInfo* di, BwdArgs a, int* parts) {
   if constexpr (kBF16) {
     if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 256, 1, true>(di, a, parts);
     // few rows: a block each, and half the columns a thread, whose code is
-    // shorter to fetch and run once (layer norms, us: 64 x 4096 10.1 -> 5.8,
-    // 1200 x 4096 17.2 -> 13.2, 1200 x 2048 10.8 -> 8.8, 300 x 1024
-    // 7.9 -> 5.7; it loses where narrow rows are many, 700 x 1024 7.1 -> 7.5,
-    // and on long runs, 8192 x 4096 56.5 -> 58.9).  Rows off their 16 bytes
-    // take it at any count: their masks cost registers that 16 columns do not
-    // leave (8192 x 1537 38.3 -> 34.8; 4096 x 2049 31.4 -> 32.5, RMS 25.5 -> 19.1)
+    // shorter to fetch and run once (layer norms, us: 148 x 2048 9.9 -> 5.7,
+    // 300 x 4096 8.9 -> 7.3, 1200 x 2048 10.8 -> 8.8, 1700 x 4096 15.9 -> 15.6,
+    // 300 x 1024 6.3 -> 5.8; it loses where narrow rows are many, 700 x 1024
+    // 7.1 -> 7.5, and on long runs).  Rows off their 16 bytes take it at any
+    // count: their masks cost registers that 16 columns do not leave (8192 x
+    // 1537 38.3 -> 33.6; 4096 x 2049 27.9 -> 31.3, but RMS 20.5 -> 19.1)
     if (held <= 4096 && (held <= 1024 ? a.rows <= 3 * di->sm_count
                                       : kShift || a.rows <= 12 * di->sm_count))
       return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 512, 1, true>(di, a, parts);
     if (held <= 512) return norm_bwd_row<kBF16, kRms, kShift, 16, 2, 256, 2, true>(di, a, parts);
-    if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 256, 2, true>(di, a, parts);
+    // a row a block where a block has no room for two: the group's size is then
+    // the block's (layer 4096 x 4096 31.0 -> 25.2 us)
+    if (held <= 2048) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 256, 2, true>(di, a, parts);
+    if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 256, 2, true>(di, a, parts);
     if (held <= 8192) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 512, 1, true>(di, a, parts);
   } else {
     if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 512, 1, true>(di, a, parts);
