@@ -11,12 +11,19 @@
 // again.  A table of the tensors travels in the kernel's parameters, so a call
 // copies nothing to the device and can be captured.
 //
+// Measured on a B200 (us; in brackets the floor at 6.55 TB/s with one read):
+// the 448 adapter gradients of a stack of 32 blocks at rank 64, 320 MB: 160 (98;
+// 147 with both reads from memory); at rank 16: 39 (24); the four of one layer:
+// 5.4 (0.3; two launches).
+//
 // Sums: eight (bf16) or four (float32) squares are added in float32, which is
 // exact enough while the sum stays away from the ends of float32's range, and
 // in float64 otherwise; everything above one 16-byte vector is float64.  So
 // neither gradients near 1e-30 nor near 1e30 spoil the norm.  The blocks'
 // sums are joined in a fixed order: the result does not depend on the
 // schedule.
+#include <algorithm>
+
 #include "elem.cuh"
 #include "internal.h"
 #include "ptx.cuh"
@@ -29,7 +36,16 @@ constexpr int kClipVecs = 4;        // 16-byte vectors of a thread in a chunk
 constexpr int kClipChunk = kClipThreads * kClipVecs * 16;  // bytes
 constexpr int kClipTensors = 512;   // tensors of one launch
 constexpr int kClipFew = 32;        // the table of a launch of few tensors: its parameters take less time to arrive
-constexpr int kClipBlocks = 592;    // four per SM of a B200
+// Blocks an SM (of a B200's 148): five for long runs (48 registers); four, and
+// the registers that the norm asks for, where a block has no more than four
+// chunks, which also lets the second kernel's blocks in beside the first's (14
+// tensors of rank 16: 5.7 us against 7.8).
+constexpr int kClipMany = 5, kClipFewer = 4, kClipSms = 148;
+constexpr int kClipBlocks = kClipMany * kClipSms;
+// The last chunks of a block's run that the norm leaves in the L2 for the
+// scaling, 6 x 740 x 16 KB = 73 MB in all; what it reads before them gives way
+// first (with the fifth block, 448 tensors of rank 64: 172 -> 160 us).
+constexpr uint32_t kClipKeep = 6;
 
 template <int kTensors>
 struct ClipTable {
@@ -79,7 +95,7 @@ __device__ __forceinline__ double square_sum(const float (&v)[kN]) {
 
 // Elements [e0, e1) of a tensor, at most a chunk.
 template <bool kBF16>
-__device__ __forceinline__ double chunk_square_sum(const void* p, int64_t e0, int64_t e1) {
+__device__ __forceinline__ double chunk_square_sum(const void* p, int64_t e0, int64_t e1, bool keep) {
   constexpr int kV = kVec<kBF16>;
   const uint4* v = static_cast<const uint4*>(p) + e0 / kV;  // chunks begin on whole vectors
   const int n = static_cast<int>(e1 - e0), whole = n / kV;
@@ -87,7 +103,8 @@ __device__ __forceinline__ double chunk_square_sum(const void* p, int64_t e0, in
   uint4 q[kClipVecs];
 #pragma unroll
   for (int k = 0; k < kClipVecs; ++k)
-    if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole) q[k] = v[threadIdx.x + k * kClipThreads];
+    if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole)
+      q[k] = keep ? v[threadIdx.x + k * kClipThreads] : __ldcs(v + threadIdx.x + k * kClipThreads);
 #pragma unroll
   for (int k = 0; k < kClipVecs; ++k) {
     if (static_cast<int>(threadIdx.x) + k * kClipThreads < whole) {
@@ -138,8 +155,8 @@ __device__ __forceinline__ void chunk_elements(const ClipTable<kTensors>& t, int
 
 // part[b] = this block's share (added to what an earlier launch of the call
 // left there when `add`).
-template <int kTensors>
-__global__ void __launch_bounds__(kClipThreads)
+template <int kTensors, int kMinBlocks>
+__global__ void __launch_bounds__(kClipThreads, kMinBlocks)
     clip_norm_kernel(const __grid_constant__ ClipTable<kTensors> t, double* __restrict__ part, bool add) {
   pdl_trigger();
   pdl_wait();
@@ -153,7 +170,8 @@ __global__ void __launch_bounds__(kClipThreads)
       while (t.end[i] <= c) ++i;
       int64_t e0, e1;
       chunk_elements(t, i, c, e0, e1);
-      acc += t.bf16[i] ? chunk_square_sum<true>(t.in[i], e0, e1) : chunk_square_sum<false>(t.in[i], e0, e1);
+      const bool keep = c + kClipKeep >= c1;
+      acc += t.bf16[i] ? chunk_square_sum<true>(t.in[i], e0, e1, keep) : chunk_square_sum<false>(t.in[i], e0, e1, keep);
     }
   }
   acc = block_sum(acc, red);
@@ -223,25 +241,25 @@ cudaError_t clip_grads_t(int n, const void* const* grads, const falqon_dtype* dt
                          float max_norm, float factor, void* const* outs, float* norm, float* coef,
                          int32_t* dev_status, double* part, cudaStream_t stream) {
   ClipTable<kTensors> t;
-  auto grid_of = [&]() {
-    return t.chunks < static_cast<uint32_t>(kClipBlocks) ? (t.chunks ? t.chunks : 1u) : static_cast<unsigned>(kClipBlocks);
+  auto many = [&]() { return t.chunks > 4u * kClipBlocks; };
+  auto grid_of = [&]() -> unsigned {
+    return many() ? kClipBlocks : std::min<unsigned>(std::max(t.chunks, 1u), kClipFewer * kClipSms);
   };
   int parts = 0;
   for (int i = 0; i < n || parts == 0;) {  // at least one launch: no elements at all give norm 0
     i = clip_table(t, i, n, grads, outs, dtypes, numel);
     // the first launch sets how many sums there are; later ones add to them
     const unsigned grid = parts ? static_cast<unsigned>(parts) : (i < n ? kClipBlocks : grid_of());
-    cudaError_t e =
-        launch_pdl(clip_norm_kernel<kTensors>, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts != 0);
+    auto kernel = many() ? clip_norm_kernel<kTensors, kClipMany> : clip_norm_kernel<kTensors, 1>;
+    cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kClipThreads), 0, stream, 1u, t, part, parts != 0);
     if (e != cudaSuccess) return e;
     parts = static_cast<int>(grid);
   }
   bool first = true;
   for (int i = 0; i < n || first;) {
     i = clip_table(t, i, n, grads, outs, dtypes, numel);
-    cudaError_t e = launch_pdl(clip_scale_kernel<kTensors>, dim3(outs ? grid_of() : 1u), dim3(kClipThreads), 0, stream,
-                               1u, t, part, parts, max_norm, factor, outs != nullptr, first ? norm : nullptr, coef,
-                               dev_status);
+    cudaError_t e = launch_pdl(clip_scale_kernel<kTensors>, dim3(outs ? grid_of() : 1u), dim3(kClipThreads), 0, stream, 1u, t, part, parts,
+                               max_norm, factor, outs != nullptr, first ? norm : nullptr, coef, dev_status);
     if (e != cudaSuccess) return e;
     first = false;
     if (!outs) break;
