@@ -12,6 +12,10 @@
 // matrix gives a warp several rows at once.  The blocks' sums are joined in a
 // fixed order by a second kernel, so the gradients do not depend on the
 // schedule.
+//
+// Measured on a B200 (us; in brackets the floor at 6.55 TB/s), GELU: 8192 x
+// 11008 86.5 (82.6), 4096 x 4096 19.5 to 20 (15.4); SiLU, 200 x 272: 3.2 (0.05;
+// two launches).
 #include "act.cuh"
 #include "elem.cuh"
 #include "internal.h"
