@@ -22,7 +22,7 @@
 //   backward  8192 x 4096 bf16 + dres   RMS 44.9, layer 47.8 (41.0)
 //             4096 x 4096 bf16   RMS 21.4, layer 25.2 (15.4)
 //             4096 x 4096 fp32   RMS 34.2, layer 36.9 (30.7)
-//             8192 x 1537 bf16   RMS 24.4, layer 33.6 (11.5)
+//             8192 x 1537 bf16   RMS 24.3, layer 33.6 (11.5)
 //              300 x 4096 bf16   RMS 6.0, layer 7.3 (1.1)
 // (the backward with its second kernel, which joins the blocks' sums over the
 // rows: about 2.5 us).  float32 is near its bound; in bf16 the backward's
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // flight, stays at 8.  The rows streamed through a ring in shared memory by
 // bulk copies instead took 26.6 (RMS) and 36.1 us (layer).
 //
-// kMode: a block takes a row (0), a group of `group_threads` threads (1) or a
-// warp (2); where a block holds several groups it joins their sums at the end.
+// kMode: a block takes a row (0), a group of kTpr threads (1) or a warp (2);
+// where a block holds several groups it joins their sums at the end.
 constexpr int kMaxGroups = 15;  // a named barrier each beside the block's
 constexpr int kL2Rows = 2;      // rows ahead that are asked for into L2
 
@@ -408,13 +408,12 @@ __device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
   return v;
 }
 
-template <bool kBF16, bool kRms, bool kShift, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
+template <bool kBF16, bool kRms, bool kShift, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead, int kTpr>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     norm_bwd_row_kernel(const void* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ gamma,
                         bool param_bf16, const float* __restrict__ mean, const float* __restrict__ rstd,
                         const void* __restrict__ dres, int64_t rows, int64_t cols, void* __restrict__ dx,
-                            float* __restrict__ part_g, float* __restrict__ part_b, int32_t* __restrict__ dev_status,
-                        int group_threads) {
+                            float* __restrict__ part_g, float* __restrict__ part_b, int32_t* __restrict__ dev_status) {
   using U = Unit<kBF16, kShift>;
   constexpr int kN = kCols / U::V, kPairs = U::Pairs;
   constexpr bool kKeep = kAhead;           // gamma in registers
@@ -435,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
   pdl_wait();
   const float inv = 1.0f / static_cast<float>(cols);
   const int lane = threadIdx.x & 31;
-  const int tpr = kMode == 2 ? 32 : kMode == 1 ? group_threads : static_cast<int>(blockDim.x);
+  const int tpr = kMode == 2 ? 32 : kMode == 1 ? kTpr : static_cast<int>(blockDim.x);
   const int groups = kMode == 0 ? 1 : static_cast<int>(blockDim.x) / tpr;
   const int group = kMode == 0 ? 0 : static_cast<int>(threadIdx.x) / tpr;
   const int t = static_cast<int>(threadIdx.x) - group * tpr, warp = t >> 5;
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
           if (lane == 16) r[kRow + warp] = c2;
         if constexpr (kMode == 0) __syncthreads();
         else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-        constexpr int kWarps = kMode == 1 ? 8 : kThreads / 32;  // a group of several has at most 256 threads
+        constexpr int kWarps = kMode == 1 ? (kTpr + 127) / 128 * 4 : kThreads / 32;  // a multiple of four
         c2 = sum_warps<kWarps>(r);
         if constexpr (!kRms) c1 = sum_warps<kWarps>(r + kRow);
       }
@@ -755,10 +754,10 @@ void norm_bwd_outputs(BwdArgs& a, int parts) {
   }
 }
 
-template <bool kBF16, bool kRms, bool kShift, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead>
+template <bool kBF16, bool kRms, bool kShift, int kCols, int kMode, int kThreads, int kBlocks, bool kAhead, int kTpr = 0>
 cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
-  auto kernel = norm_bwd_row_kernel<kBF16, kRms, kShift, kCols, kMode, kThreads, kBlocks, kAhead>;
-  const int tpr = kMode == 2 ? 32 : row_threads<kBF16, kShift>(a.cols, kCols);
+  auto kernel = norm_bwd_row_kernel<kBF16, kRms, kShift, kCols, kMode, kThreads, kBlocks, kAhead, kTpr>;
+  const int tpr = kTpr ? kTpr : kMode == 2 ? 32 : row_threads<kBF16, kShift>(a.cols, kCols);
   int groups = kMode == 0 ? 1 : std::min(kThreads / tpr, kMaxGroups);
   // few rows: one a group
   const int64_t sms = di->sm_count;
@@ -772,7 +771,7 @@ cudaError_t norm_bwd_row(const DeviceInfo* di, BwdArgs a, int* parts) {
   *parts = static_cast<int>(blocks);
   norm_bwd_outputs(a, *parts);
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(groups * tpr), 0, a.stream, 1u, a.dy, a.x,
-                    a.gamma, a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, a.dev_status, tpr);
+                    a.gamma, a.param_bf16, a.mean, a.rstd, a.dres, a.rows, a.cols, a.dx, a.part_g, a.part_b, a.dev_status);
 }
 
 template <bool kBF16, bool kRms, bool kShift>
@@ -781,25 +780,32 @@ cudaError_t norm_bwd_rows(const DeviceInfo* di, BwdArgs a, int* parts) {
   const int64_t held = a.cols + kSlack;
   if constexpr (kBF16) {
     if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 256, 1, true>(di, a, parts);
-    // few rows: a block each, and half the columns a thread, whose code is
-    // shorter to fetch and run once (layer norms, us: 148 x 2048 9.9 -> 5.7,
-    // 300 x 4096 8.9 -> 7.3, 1200 x 2048 10.8 -> 8.8, 1700 x 4096 15.9 -> 15.6,
-    // 300 x 1024 6.3 -> 5.8; it loses where narrow rows are many, 700 x 1024
-    // 7.1 -> 7.5, and on long runs).  Rows off their 16 bytes take it at any
-    // count: their masks cost registers that 16 columns do not leave (8192 x
-    // 1537 38.3 -> 33.6; 4096 x 2049 27.9 -> 31.3, but RMS 20.5 -> 19.1)
-    if (held <= 4096 && (held <= 1024 ? a.rows <= 3 * di->sm_count
-                                      : kShift || a.rows <= 12 * di->sm_count))
+    // A block a row and 8 columns a thread: few rows, since the code is shorter
+    // to fetch and run once (layer norms, us: 148 x 2048 9.9 -> 5.7, 300 x 4096
+    // 8.9 -> 7.3, 1700 x 4096 15.9 -> 15.6, 300 x 1024 6.3 -> 5.8; it loses where
+    // narrow rows are many, 700 x 1024 7.1 -> 7.5, and on long runs); the widths
+    // whose groups of 16 columns a thread are two a block, at any count (8192 x
+    // 2048 28.6 -> 27.4, 8192 x 1792 28.4 -> 26.2); and rows off their 16 bytes,
+    // whose masks cost registers that 16 columns do not leave (8192 x 1537
+    // 38.3 -> 33.6; 4096 x 2049 27.9 -> 31.3, but RMS 20.5 -> 19.1).
+    const bool few = a.rows <= (held <= 1024 ? 3 : 12) * static_cast<int64_t>(di->sm_count);
+    if (held <= 4096 && (few || (held > 1536 && held <= 2048) || (kShift && held > 1024)))
       return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 512, 1, true>(di, a, parts);
     if (held <= 512) return norm_bwd_row<kBF16, kRms, kShift, 16, 2, 256, 2, true>(di, a, parts);
-    // a row a block where a block has no room for two: the group's size is then
-    // the block's (layer 4096 x 4096 31.0 -> 25.2 us)
-    if (held <= 2048) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 256, 2, true>(di, a, parts);
+    // groups of a size known when compiled (layer 8192 x 1536 25.4 -> 23.1 us,
+    // 16384 x 1000 27.6 -> 25.9), and one a block where a block has no room for
+    // two (4096 x 4096 31.0 -> 25.2)
+    if (held <= 1024) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 256, 2, true, 64>(di, a, parts);
+    if (held <= 1536) return norm_bwd_row<kBF16, kRms, kShift, 16, 1, 192, 2, true, 96>(di, a, parts);
     if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 256, 2, true>(di, a, parts);
     if (held <= 8192) return norm_bwd_row<kBF16, kRms, kShift, 16, 0, 512, 1, true>(di, a, parts);
   } else {
     if (held <= 256) return norm_bwd_row<kBF16, kRms, kShift, 8, 2, 512, 1, true>(di, a, parts);
-    if (held <= 2048) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 512, 1, true>(di, a, parts);
+    if (held <= 512) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 512, 1, true, 64>(di, a, parts);
+    if (held <= 768) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 480, 1, true, 96>(di, a, parts);
+    if (held <= 1024) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 512, 1, true, 128>(di, a, parts);
+    if (held <= 1536) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 384, 1, true, 192>(di, a, parts);
+    if (held <= 2048) return norm_bwd_row<kBF16, kRms, kShift, 8, 1, 512, 1, true, 256>(di, a, parts);
     if (held <= 4096) return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 512, 1, true>(di, a, parts);
     if (held <= 8192) return norm_bwd_row<kBF16, kRms, kShift, 8, 0, 1024, 1, true>(di, a, parts);
   }

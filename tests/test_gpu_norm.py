@@ -55,6 +55,9 @@ def _check_fwd(x, gamma, beta, eps, rms, y, mean, rstd):
 
 SHAPES = [(1, 1), (1, 4096), (3, 8), (5, 17), (33, 257), (300, 1000), (65, 2050), (4, 16384), (2, 40001), (1000, 512),
           (9, 8192), (37, 12288), (3, 20000), (2, 65536)]
+# more rows than the device holds at once, in each class of row lengths
+MANY_ROWS = [(2000, 400), (2000, 515), (1900, 700), (1900, 1000), (1900, 1003), (1900, 1280), (1900, 1531),
+             (1900, 1792), (1900, 1801), (1900, 2056), (1900, 3001), (1900, 4096)]
 
 
 @pytest.mark.parametrize("rms", [False, True])
@@ -145,7 +148,7 @@ def _check_bwd(x, gamma, dy, dres, mean, rstd, rms, dx, dgamma, dbeta):
 
 @pytest.mark.parametrize("rms", [False, True])
 @pytest.mark.parametrize("dtype,pdtype", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
-@pytest.mark.parametrize("rows,cols", SHAPES + [(2000, 64), (1500, 24), (700, 1536)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(2000, 64), (1500, 24), (700, 1536)] + MANY_ROWS)
 def test_backward(cuda_device, rows, cols, dtype, pdtype, rms):
     x, gamma, beta, dy, dres = _make(rows * 3 + cols, rows, cols, dtype, pdtype, True, rms)
     kind = F.NORM_RMS if rms else F.NORM_LAYER
