@@ -16,9 +16,9 @@
 // sums and its outputs, so it is read once; the threads that share it meet at
 // one barrier for each sum that the next step waits for.  Measured on a B200
 // (us, floor at 6.55 TB/s in brackets):
-//   forward   4096 x 4096 bf16   RMS 12.9, layer 15.4 (10.2)
-//             4096 x 4096 fp32   RMS 23.2, layer 24.4 (20.5)
-//             8192 x 1537 bf16   RMS 12.8, layer 19.4 (7.7)
+//   forward   4096 x 4096 bf16   RMS 12.8, layer 14.7 (10.2)
+//             4096 x 4096 fp32   RMS 23.4, layer 24.4 (20.5)
+//             8192 x 1537 bf16   RMS 12.1, layer 18.7 (7.7)
 //   backward  8192 x 4096 bf16 + dres   RMS 44.9, layer 47.8 (41.0)
 //             4096 x 4096 bf16   RMS 21.4, layer 25.2 (15.4)
 //             4096 x 4096 fp32   RMS 34.2, layer 36.9 (30.7)
@@ -78,17 +78,7 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Sum of a row of per-warp values, zeros past the last (a multiple of four are read).
-__device__ __forceinline__ float sum_warps(const float* r, int warps) {
-  float s = 0.0f;
-  for (int i = 0; i < warps; i += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(r + i);
-    s += (v.x + v.y) + (v.z + v.w);
-  }
-  return s;
-}
-
-// The same for a number known when compiled.
+// Sum of a row of kWarps per-warp values, zeros past the last (a multiple of four are read).
 template <int kWarps>
 __device__ __forceinline__ float sum_warps(const float* r) {
   float s = 0.0f;
@@ -115,7 +105,7 @@ __device__ __forceinline__ void prefetch_l2(const uint8_t* p, int64_t bytes, con
 // thread, in an order that depends on their number alone.  Calls of a block
 // alternate between two buffers: a thread that writes one again has passed the
 // barrier of the call between, which every thread reaches after its reads.
-template <bool kWarp>
+template <bool kWarp, int kWarps>
 __device__ __forceinline__ float row_sum(float v, float (*red)[32], uint32_t& turn) {
   v = warp_sum(v);
   if constexpr (!kWarp) {
@@ -124,7 +114,7 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[32], uint32_t& tu
     ++turn;
     if (lane == 0) r[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = sum_warps(r, static_cast<int>(blockDim.x >> 5));
+    v = sum_warps<kWarps>(r);
   }
   return v;
 }
@@ -236,8 +226,10 @@ struct Unit {
   }
 };
 
-template <bool kBF16, bool kRms, bool kShift, int kCols, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 128 : 1024)
+// (0 blocks: no bound on the registers; a bound of one lets it take more than
+// four blocks of 256 threads an SM leave)
+template <bool kBF16, bool kRms, bool kShift, int kCols, bool kWarp, int kThreads>
+__global__ void __launch_bounds__(kThreads, kShift && !kRms && !kWarp ? 1024 / kThreads : 0)
     norm_fwd_row_kernel(const void* __restrict__ x, const void* __restrict__ gamma, const void* __restrict__ beta,
                         bool param_bf16, int64_t rows, int64_t cols, float eps, void* __restrict__ y,
                         float* __restrict__ mean, float* __restrict__ rstd, int32_t* __restrict__ dev_status) {
@@ -292,7 +284,7 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
           for (int j = 0; j < kPairs; ++j) s = add2(s, v[j]);
         }
       }
-      mu = row_sum<kWarp>(s.x + s.y, red, turn) * inv;
+      mu = row_sum<kWarp, kThreads / 32>(s.x + s.y, red, turn) * inv;
     }
     float2 q = both(0.0f);
 #pragma unroll
@@ -309,7 +301,7 @@ __global__ void __launch_bounds__(kWarp ? 128 : 1024)
         for (int j = 0; j < kPairs; ++j) q = fma2(v[j], v[j], q);
       }
     }
-    const float rs = 1.0f / sqrtf(row_sum<kWarp>(q.x + q.y, red, turn) * inv + eps);
+    const float rs = 1.0f / sqrtf(row_sum<kWarp, kThreads / 32>(q.x + q.y, red, turn) * inv + eps);
     if (t == 0) {
       if (mean && !kRms) mean[row] = mu;
       if (rstd) rstd[row] = rs;
@@ -690,9 +682,9 @@ int64_t row_blocks(int64_t rows, int64_t groups, int64_t resident) {
   return kShift ? std::max<int64_t>(resident / kVec<kBF16> * kVec<kBF16>, kVec<kBF16>) : resident;
 }
 
-template <bool kBF16, bool kRms, bool kShift, int kCols, bool kWarp>
+template <bool kBF16, bool kRms, bool kShift, int kCols, bool kWarp, int kThreads>
 cudaError_t norm_fwd_row(const DeviceInfo* di, const FwdArgs& a, int threads) {
-  auto kernel = norm_fwd_row_kernel<kBF16, kRms, kShift, kCols, kWarp>;
+  auto kernel = norm_fwd_row_kernel<kBF16, kRms, kShift, kCols, kWarp, kThreads>;
   static int cache[33] = {};
   int per_sm = 1;
   cudaError_t e = resident_blocks(kernel, threads, cache, &per_sm);
@@ -707,15 +699,24 @@ template <bool kBF16, bool kRms, bool kShift>
 cudaError_t norm_fwd_rows(const DeviceInfo* di, const FwdArgs& a, bool* taken) {
   constexpr int kSlack = kShift ? kVec<kBF16> - 1 : 0;
   *taken = true;
-  if (a.cols + kSlack <= 256) return norm_fwd_row<kBF16, kRms, kShift, 8, true>(di, a, 128);
-  if (a.cols + kSlack <= 512) return norm_fwd_row<kBF16, kRms, kShift, 16, true>(di, a, 128);
+  if (a.cols + kSlack <= 256) return norm_fwd_row<kBF16, kRms, kShift, 8, true, 128>(di, a, 128);
+  if (a.cols + kSlack <= 512) return norm_fwd_row<kBF16, kRms, kShift, 16, true, 128>(di, a, 128);
   // 16 columns a thread where they and their parameters fit 64 registers
   // (bf16), else 8: 4096 x 4096 bf16 layer 15.5 against 20.3 us, but float32
-  // 32.1 against 24.1.
+  // 32.1 against 24.1.  Compiled for at most so many threads, whose sums are
+  // then read without a loop (4096 x 4096 bf16 layer 15.4 -> 14.7); layer norms
+  // off their 16 bytes are held to 64 registers (8192 x 2050 25.5 -> 23.5).
   auto threads = [&](int c) { return row_threads<kBF16, kShift>(a.cols, c); };
-  if constexpr (!kBF16)
-    if (threads(8) <= 1024) return norm_fwd_row<kBF16, kRms, kShift, 8, false>(di, a, threads(8));
-  if (threads(16) <= 1024) return norm_fwd_row<kBF16, kRms, kShift, 16, false>(di, a, threads(16));
+  if constexpr (!kBF16) {
+    if (threads(8) <= 256) return norm_fwd_row<kBF16, kRms, kShift, 8, false, 256>(di, a, threads(8));
+    if (threads(8) <= 512) return norm_fwd_row<kBF16, kRms, kShift, 8, false, 512>(di, a, threads(8));
+    if (threads(8) <= 1024) return norm_fwd_row<kBF16, kRms, kShift, 8, false, 1024>(di, a, threads(8));
+  } else {
+    if (threads(16) <= 128) return norm_fwd_row<kBF16, kRms, kShift, 16, false, 128>(di, a, threads(16));
+    if (threads(16) <= 256) return norm_fwd_row<kBF16, kRms, kShift, 16, false, 256>(di, a, threads(16));
+    if (threads(16) <= 512) return norm_fwd_row<kBF16, kRms, kShift, 16, false, 512>(di, a, threads(16));
+  }
+  if (threads(16) <= 1024) return norm_fwd_row<kBF16, kRms, kShift, 16, false, 1024>(di, a, threads(16));
   *taken = false;
   return cudaSuccess;
 }
