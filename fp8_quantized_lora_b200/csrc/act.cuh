@@ -38,6 +38,14 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// z held to [-bound, bound]; NaN for NaN.
+__device__ __forceinline__ float clamp_nan(float z, float bound) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(bound));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(-bound));
+  return y;
+}
+
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluTwoU = 1.5957691216057308f;  // 2 sqrt(2/pi)
 constexpr float kGeluCubic = 0.044715f;
@@ -109,9 +117,10 @@ __device__ __forceinline__ float2 act_slope2(float2 z) {
     return fma2(mul2(z, both(kInvSqrt2Pi)), e, make_float2(normal_cdf(z.x, h.x), normal_cdf(z.y, h.y)));
   }
   if constexpr (kAct == FALQON_ACT_GELU_TANH) {
-    // past |z| = 20 p is 0 or 1 whatever z: keeps the products finite
-    float2 z2 = mul2(z, z);
-    z2 = make_float2(fminf(z2.x, 400.0f), fminf(z2.y, 400.0f));
+    // past |z| = 20 p is 0 or 1 in float32 whatever z, and so is the slope:
+    // clamped there, no product overflows up to the largest z (NaN stays NaN)
+    z = make_float2(clamp_nan(z.x, 20.0f), clamp_nan(z.y, 20.0f));
+    const float2 z2 = mul2(z, z);
     const float2 n = mul2(z, fma2(z2, both(-kGeluTwoU * kLog2E * kGeluCubic), both(-kGeluTwoU * kLog2E)));
     return logistic_slope2(n, mul2(z, fma2(z2, both(3.0f * kGeluTwoU * kGeluCubic), both(kGeluTwoU))));
   }

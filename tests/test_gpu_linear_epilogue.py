@@ -189,6 +189,24 @@ def test_backward(cuda_device, M, N, which):
         assert torch.equal(F.falqon_linear_epilogue_bwd(dy, None, which, dz=None)[1], dbias)
 
 
+@pytest.mark.parametrize("which", range(1, 5))
+def test_backward_up_to_the_largest_pre_activation(cuda_device, which):
+    """Past |z| = 1000 every slope is 1 or 0 (the rest is below 1e-400), so dz is dy or 0 without a rounding, and
+    the sums of a few powers of two are exact; a NaN stays one."""
+    big = torch.tensor([1e3, 1e10, 1.8e19, 1e25, 1e30, 3.8e36, 4e36, 1e37, 1e38, 3.3e38, 3.38e38], device="cuda")
+    z = torch.zeros(70, 32, device="cuda")
+    z[:, :11], z[:, 11:22] = big, -big
+    z = z.to(BF)
+    dy = torch.full_like(z, 2.0 ** -6)
+    dz, dbias = F.falqon_linear_epilogue_bwd(dy, z, which)
+    assert torch.equal(dz[:, :11], dy[:, :11]) and (dz[:, 11:22] == 0).all()
+    assert (dbias[:11] == 70 * 2.0 ** -6).all() and (dbias[11:22] == 0).all()
+    z[3, 5] = math.nan
+    if which != 1:  # ReLU's slope is a comparison
+        dz, dbias = F.falqon_linear_epilogue_bwd(dy, z, which)
+        assert torch.isnan(dz[3, 5]) and torch.isnan(dbias[5]) and int(torch.isnan(dz).sum()) == 1
+
+
 def test_gradient_against_differences(cuda_device):
     """The slope that the backward applies against differences of the forward's own activation: N(0, 1)
     pre-activations, one sample per element.  The forward's outputs are bf16, so the differences are taken of the
