@@ -201,6 +201,34 @@ def test_backward_non_finite_row(cuda_device, cols):
             assert not torch.isfinite(dx[4]).all() and torch.isfinite(dgamma[:cols - 1]).all()
 
 
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("scale", [1e-30, 1e-20, 1e16, 1e18, 1e30])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(7, 200), (9, 515), (700, 1000), (500, 1536), (9, 4096), (2000, 4096), (3, 8192),
+                                       (3, 12001), (3, 20000)])
+def test_backward_far_magnitudes(cuda_device, rows, cols, dtype, scale, rms):
+    """Statistics far from 1, whose squares leave float32 while no term of the gradients does.  The tolerance is that
+    of the other sizes and, since dx goes down to 1e-36 and its small elements below the normal range, the absolute
+    half step there: 2^-134 for a bf16 output, 2^-150 for a float32 one and for each float32 intermediate: b (two
+    products), the sum with it, the sum with xh a, the sum with dres, and a (two products), which xh multiplies."""
+    x, gamma, beta, dy, dres = _make(rows + cols, rows, cols, dtype, F32, True, rms)
+    x, dy = (x.double() * scale).to(dtype), (dy.double() * 1e-4).to(dtype)
+    dres = (dres.double() * 1e-4 / scale).to(dtype)
+    _, mean, rstd = block.norm_fwd(x, gamma, beta, 0.0, rms)
+    mean, rstd = None if rms else mean.float(), rstd.float()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dx, dgamma, dbeta = F.falqon_norm_bwd(dy, x, gamma, mean, rstd, F.NORM_RMS if rms else F.NORM_LAYER, dres=dres,
+                                          dev_status=st)
+    _check_bwd(x, gamma, dy, dres, mean, rstd, rms, None, dgamma, dbeta)
+    xh = (x.double() if rms else x.double() - mean.double()[:, None]).abs() * rstd.double()[:, None]
+    tiny = (2.0 ** -134 if dtype == BF else 2.0 ** -150) + (5 + 2 * xh) * 2.0 ** -150
+    DX = block.norm_bwd(dy, x, gamma, mean, rstd, dres, rms)[0]
+    off = dx.double() - DX
+    rest = off.sign() * (off.abs() - tiny).clamp_min(0)  # beyond the absolute part
+    _check_bwd(x, gamma, dy, dres, mean, rstd, rms, DX + rest, None, None)
+    assert int(st.item()) == 0
+
+
 def test_gradient_agrees_with_autograd(cuda_device):
     """The whole chain x -> y -> loss against torch's differentiation of the definition in float64."""
     for rms in (False, True):
