@@ -531,6 +531,7 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 256;
 bool known_dtype(falqon_dtype d) { return d == FALQON_DTYPE_BF16 || d == FALQON_DTYPE_F32; }
 bool known_act(falqon_act a) { return a >= FALQON_ACT_NONE && a <= FALQON_ACT_SILU; }
 bool unaligned16(const void* p) { return !aligned16(p); }  // null counts as aligned
+bool unaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 falqon_status norm_shape(falqon_dtype dtype, falqon_dtype param_dtype, falqon_norm kind, int64_t rows, int64_t cols) {
   if (!known_dtype(dtype) || !known_dtype(param_dtype)) return FALQON_ERR_INVALID_ARG;
@@ -598,6 +599,21 @@ falqon_status clip_overlaps(int n, const void* const* grads, const falqon_dtype*
     if (s->index != i || s->begin != b) return FALQON_ERR_INVALID_ARG;
   }
   return FALQON_OK;
+}
+
+// norm and coef (nullable), one float each, may lie in no gradient and no
+// output, nor be the same.
+bool clip_results_overlap(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
+                          void* const* outs, const float* norm, const float* coef) {
+  const Bytes results[2] = {{norm, sizeof(float)}, {coef, sizeof(float)}};
+  if (overlap(results[0], results[1])) return true;
+  for (int i = 0; i < n; ++i) {
+    if (numel[i] == 0) continue;
+    const size_t bytes = bytes_of(dtypes[i], numel[i]);
+    for (const Bytes& r : results)
+      if (overlap(r, {grads[i], bytes}) || (outs && overlap(r, {outs[i], bytes}))) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -711,8 +727,10 @@ falqon_status falqon_clip_grads(int n, const void* const* grads, const falqon_dt
     falqon_status s = clip_overlaps(n, grads, dtypes, numel, outs);
     if (s != FALQON_OK) return s;
   }
+  if (unaligned4(norm) || unaligned4(coef)) return FALQON_ERR_UNSUPPORTED;
   falqon_status s = check_ws(clip_workspace_bytes(), workspace, workspace_bytes);
   if (s != FALQON_OK) return s;
+  if (clip_results_overlap(n, grads, dtypes, numel, outs, norm, coef)) return FALQON_ERR_INVALID_ARG;
   if (!current_device_info()) return FALQON_ERR_CUDA;
   return from_cuda(launch_clip_grads(n, grads, dtypes, numel, max_norm, factor, outs, norm, coef, dev_status,
                                      workspace, static_cast<cudaStream_t>(stream)));

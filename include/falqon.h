@@ -659,7 +659,8 @@ FALQON_API falqon_status falqon_linear_epilogue_bwd(const void* dy, const void* 
  *  overlap no other gradient or output (FALQON_ERR_INVALID_ARG).  outs NULL:
  *  the norm alone.  The host arrays are read before the call returns.
  *  max_norm > 0 (INFINITY: no clipping); factor finite.
- *  norm 1 float (written; infinity above float32), coef 1 float (nullable).
+ *  norm 1 float (written; infinity above float32), coef 1 float (nullable):
+ *  4-byte aligned, as scales are, in no gradient or output, and apart.
  *  workspace: falqon_workspace_size(FALQON_OP_CLIP_GRADS, 0, 0, 0, 0) bytes.
  *  Requirements: numel[i] <= 2^42; fewer than 2^31 chunks of 4096 elements.
  *  Launches: two for up to 512 tensors that hold elements, two more for each

@@ -161,6 +161,25 @@ def test_clip_refuses_overlapping_outputs():
     assert _clip(ptrs=(A, A + 208), outs=(A, A + 208), numel=(104, 8), dtypes=(BF, BF), ws=None, wsb=0) == 3
 
 
+def test_clip_refuses_results_over_tensors_or_one_another():
+    """norm and coef are outputs like the others: each at the first and the last float of a gradient, of an output,
+    and in one place, with and without outputs."""
+    A, B, O, Q, R = (v << 20 for v in (1, 2, 3, 4, 5))
+    ws = C.c_void_p(1 << 28)
+    vp = lambda v: None if v is None else (C.c_void_p * len(v))(*v)  # noqa: E731
+    dtypes, numel = (C.c_int * 2)(BF, F32), (C.c_int64 * 2)(100, 50)  # 200 bytes each
+
+    def call(norm, coef=None, outs=None):
+        return F.lib().falqon_clip_grads(2, vp((A, B)), dtypes, numel, 1.0, 1.0, vp(outs), C.c_void_p(norm),
+                                         None if coef is None else C.c_void_p(coef), None, ws, 1 << 20, None)
+    for outs in (None, (O, Q), (A, B)):
+        assert call(R, R, outs) == 1
+        for begin in (A, B) + (outs or ()):
+            for at in (begin, begin + 196):
+                assert call(at, R, outs) == 1 and call(R, at, outs) == 1 and call(at, None, outs) == 1
+        assert call(R + 2, None, outs) == 2 and call(R, R + 5, outs) == 2
+
+
 def test_binding_refuses_wrong_tensors():
     x = torch.zeros(4, 16, dtype=torch.bfloat16)
     for call in (lambda: F.falqon_norm_fwd(x), lambda: F.falqon_norm_fwd(x[0]),

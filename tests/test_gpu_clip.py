@@ -130,6 +130,25 @@ def test_refusals(cuda_device):
     assert abs(norm.item() - math.sqrt(128)) < 1e-5
 
 
+def test_results_beside_the_gradients(cuda_device):
+    """norm and coef right behind a gradient and right before the next are apart; on one of their elements, or in one
+    place, they are refused."""
+    flat = torch.zeros(1000, device="cuda")
+    a, norm, coef, b = flat[:100], flat[100:101], flat[103:104], flat[104:200]
+    keep = [t.copy_(torch.randn(t.numel(), device="cuda")).clone() for t in (a, b)]
+    for out in (None, True, [a, b]):
+        for t, k in zip((a, b), keep):
+            t.copy_(k)
+        outs = F.falqon_clip_grads([a, b], 1.0, 2.0, out=out, norm=norm, coef=coef)[0]
+        _check(keep, 1.0, 2.0, outs, norm, coef)
+        assert (flat[101:103] == 0).all() and (flat[200:] == 0).all()
+        for at in (a[:1], a[99:], b[:1], b[95:]):
+            for kw in (dict(norm=at), dict(norm=norm, coef=at), dict(norm=norm, coef=norm)):
+                with pytest.raises(F.FalqonError) as e:
+                    F.falqon_clip_grads([a, b], 1.0, 2.0, out=out, **kw)
+                assert e.value.status == 1
+
+
 def test_more_than_2_31_elements(cuda_device):
     n = (1 << 31) + 12345
     g = torch.zeros(n, dtype=BF, device="cuda")
