@@ -691,10 +691,8 @@ def falqon_linear_epilogue_bwd(dy, z, act, dz=True, dbias=True, workspace=None, 
     return dz, dbias
 
 
-class GradList:
-    """Tensors (bf16 or float32, contiguous, on one device) marshalled once for
-    falqon_clip_grads: a training loop whose gradient buffers stay where they
-    are builds it at its start.  Keeps the tensors alive."""
+class _Tensors:
+    """Tensors (bf16 or float32, contiguous, on one device) marshalled for one call."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -711,11 +709,53 @@ class GradList:
         self.numel = (C.c_int64 * n)(*[t.numel() for t in self.tensors])
         self.dtypes = (C.c_int * n)(*[_DTYPES[t.dtype] for t in self.tensors])
 
+    def current(self):
+        return self
+
     def __len__(self):
         return len(self.tensors)
 
     def __iter__(self):
         return iter(self.tensors)
+
+
+class GradList(_Tensors):
+    """Tensors (bf16 or float32, contiguous, on one device) marshalled once for
+    many calls of falqon_clip_grads: a training loop whose gradient buffers stay
+    where they are builds it at its start.
+
+    The list stands for the memory that the tensors have when it is built, and
+    keeps it: gradients that get other memory later (a new .grad every step,
+    `data =`, set_) need a new list, as they need a new CUDA graph.  Memory that
+    resize_ moves is followed, memory that it gives back is refused
+    (ValueError); each call looks at the address of every storage, of which a
+    flat buffer is one."""
+
+    def __init__(self, tensors):
+        super().__init__(tensors)
+        at = {}  # storage -> its place in _storages
+        self._storages, self._where = [], []
+        for t in self.tensors:
+            s = t.untyped_storage()
+            k = at.setdefault(s._cdata, len(at))
+            if k == len(self._storages):
+                self._storages.append(s)
+            # (storage, first byte, end) of each tensor; one without elements has no memory
+            first = t.storage_offset() * t.element_size()
+            self._where.append((k, first, first + t.numel() * t.element_size()) if t.numel() else None)
+        self._bases = [s.data_ptr() for s in self._storages]
+
+    def current(self):
+        """This list, with the addresses that its memory has now."""
+        bases = [s.data_ptr() for s in self._storages]
+        if bases != self._bases:
+            sizes = [s.nbytes() for s in self._storages]
+            if any(w and w[2] > sizes[w[0]] for w in self._where):
+                raise ValueError("memory of a GradList has been given back")
+            for i, w in enumerate(self._where):
+                self.pointers[i] = bases[w[0]] + w[1] if w else None
+            self._bases = bases
+        return self
 
 
 def falqon_clip_grads(grads, max_norm, factor=1.0, out=None, norm=None, coef=None, dev_status=None, workspace=None,
@@ -725,7 +765,7 @@ def falqon_clip_grads(grads, max_norm, factor=1.0, out=None, norm=None, coef=Non
     out: None (the norm alone), True (allocate), or tensors / a GradList of the
     same sizes and types, which may be `grads` itself (in place).  Returns
     (out, norm, coef), norm and coef being float32 [1]."""
-    g = grads if isinstance(grads, GradList) else GradList(grads)
+    g = grads.current() if isinstance(grads, _Tensors) else _Tensors(grads)
     dev = g.device
     scope = _elsewhere(dev, stream)
     if scope is not None:
@@ -733,9 +773,11 @@ def falqon_clip_grads(grads, max_norm, factor=1.0, out=None, norm=None, coef=Non
             return falqon_clip_grads(g, max_norm, factor, g if out is grads else out, norm, coef, dev_status, workspace)
     o = out
     if out is True:
-        o = GradList(torch.empty_like(t) for t in g)
-    elif out is not None and not isinstance(out, GradList):
-        o = GradList(out)
+        o = _Tensors(torch.empty_like(t) for t in g)
+    elif out is grads:
+        o = g
+    elif out is not None:
+        o = out.current() if isinstance(out, _Tensors) else _Tensors(out)
     if o is not None and o is not g:
         if len(o) != len(g) or o.device != dev or bytes(o.numel) != bytes(g.numel) or \
                 bytes(o.dtypes) != bytes(g.dtypes):

@@ -180,6 +180,57 @@ def test_clip_refuses_results_over_tensors_or_one_another():
         assert call(R + 2, None, outs) == 2 and call(R, R + 5, outs) == 2
 
 
+def test_a_gradient_list_keeps_or_follows_its_memory(monkeypatch):
+    """The pointers that reach the C call, recorded in its place: always of memory that is alive, whatever became of
+    the tensors, and a refusal where that memory was given back."""
+    seen = []
+
+    class Recorder:
+        @staticmethod
+        def falqon_clip_grads(n, grads, dtypes, numel, max_norm, factor, outs, *rest):
+            seen.append([(grads[i], numel[i], None if outs is None else outs[i]) for i in range(n)])
+            return 0
+    monkeypatch.setattr(F, "lib", Recorder)
+    monkeypatch.setattr(F, "_ptr", lambda t: C.c_void_p(t.data_ptr()))
+    monkeypatch.setattr(F, "_elsewhere", lambda dev, stream: None)
+    monkeypatch.setattr(F, "_raw_stream", lambda dev: None)
+    monkeypatch.setattr(F, "falqon_workspace_size", lambda *a: 256)
+    flat = torch.zeros(64)
+    grads = [torch.zeros(40), flat[8:16], flat[24:64], torch.zeros(0)]
+    outs = [torch.zeros(n) for n in (40, 8, 40, 0)]
+    g, o = F.GradList(grads), F.GradList(outs)
+
+    def pointers(out):
+        F.falqon_clip_grads(g, 1.0, out=out)
+        return [(p, q) for p, _, q in seen[-1]]
+
+    first = [t.data_ptr() for t in grads[:3]] + [None]
+    outs_at = [t.data_ptr() for t in outs[:3]] + [None]
+    assert pointers(None) == [(p, None) for p in first] and [n for _, n, _ in seen[-1]] == [40, 8, 40, 0]
+    assert pointers(o) == list(zip(first, outs_at)) and pointers(g) == list(zip(first, first))
+    # other memory for a tensor: the list still stands for, and holds, the old
+    grads[0].data = torch.ones(40)
+    grads[1].set_(torch.ones(8))
+    again = [torch.full((40,), 2.0) for _ in range(50)]  # none of which may get the old memory
+    assert first[0] not in [t.data_ptr() for t in again]
+    assert pointers(o) == list(zip(first, outs_at))
+    # a storage that moves takes its tensors along
+    flat.resize_(1 << 18)
+    assert flat.data_ptr() != first[1] - 32
+    moved = [first[0], flat.data_ptr() + 32, flat.data_ptr() + 96, None]
+    assert pointers(None) == [(p, None) for p in moved] and pointers(o) == list(zip(moved, outs_at))
+    outs[2].resize_(1 << 18)
+    outs_at[2] = outs[2].data_ptr()
+    assert pointers(o) == list(zip(moved, outs_at))
+    # given back: refused, and so are the calls after it
+    flat.untyped_storage().resize_(0)
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            F.falqon_clip_grads(g, 1.0)
+    with pytest.raises(ValueError):
+        F.falqon_clip_grads(o, 1.0, out=g)
+
+
 def test_binding_refuses_wrong_tensors():
     x = torch.zeros(4, 16, dtype=torch.bfloat16)
     for call in (lambda: F.falqon_norm_fwd(x), lambda: F.falqon_norm_fwd(x[0]),

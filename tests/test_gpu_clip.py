@@ -130,6 +130,25 @@ def test_refusals(cuda_device):
     assert abs(norm.item() - math.sqrt(128)) < 1e-5
 
 
+def test_a_list_keeps_or_follows_its_memory(cuda_device):
+    """Tensors that get other memory leave the list's as it was; a storage that resize_ moves is followed; one that
+    is given back is refused."""
+    grads, outs = _tensors(7, [5000, 64, 777], (BF, F32)), [torch.zeros(n, device="cuda") for n in (5000, 64, 777)]
+    outs = [o.to(g.dtype) for o, g in zip(outs, grads)]
+    g, o = F.GradList(grads), F.GradList(outs)
+    keep = [t.clone() for t in grads]
+    _check(keep, 1.0, -2.0, *F.falqon_clip_grads(g, 1.0, -2.0, out=o))
+    grads[0].data = 3 * grads[0]
+    grads[1].set_(5 * grads[1])
+    fill = [torch.full((5000,), math.nan, dtype=BF, device="cuda") for _ in range(20)]  # none in the list's memory
+    grads[2].resize_(100000)
+    _check(keep, 1.0, -2.0, *F.falqon_clip_grads(g, 1.0, -2.0, out=o))
+    assert torch.equal(grads[2][:777], keep[2]) and len(fill) == 20
+    grads[2].untyped_storage().resize_(0)
+    with pytest.raises(ValueError):
+        F.falqon_clip_grads(g, 1.0)
+
+
 def test_results_beside_the_gradients(cuda_device):
     """norm and coef right behind a gradient and right before the next are apart; on one of their elements, or in one
     place, they are refused."""
