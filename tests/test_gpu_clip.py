@@ -59,6 +59,25 @@ def test_clip(cuda_device, sizes, dtypes):
         assert torch.equal(n3, norm) and all(torch.equal(a, b) for a, b in zip(inplace, outs))
 
 
+@pytest.mark.parametrize("n,size", [(40, 700000), (100, 300000), (600, 60000)])
+def test_long_runs_across_many_tensors(cuda_device, n, size):
+    """More than four 16 KB chunks a block, of odd lengths: each block's run goes on from tensor to tensor, of both
+    types; 600 tensors take two launches each way."""
+    sizes = [size + 997 * i % 4001 for i in range(n)]
+    for dtypes in ((BF, F32), (BF, BF, F32)):
+        grads = _tensors(n, sizes, dtypes)
+        chunks = sum(-(-g.numel() * g.element_size() // 16384) for g in grads)
+        assert chunks > 4 * 740
+        _, norm64, _ = block.clip_grads(grads, 1.0)
+        mn = torch.tensor(norm64 / 3, dtype=F32).item()
+        outs, norm, coef = F.falqon_clip_grads(grads, mn, -0.5, out=True)
+        _check(grads, mn, -0.5, outs, norm, coef)
+        inplace = [g.clone() for g in grads]
+        _, n2, c2 = F.falqon_clip_grads(inplace, mn, -0.5, out=inplace)
+        assert torch.equal(n2, norm) and torch.equal(c2, coef)
+        assert all(torch.equal(a, b) for a, b in zip(inplace, outs))
+
+
 def test_neighbours_stay_as_they_were(cuda_device):
     """Views of one buffer, each of an odd length: what lies between them is neither read nor written."""
     flat = torch.full((40000,), math.nan, dtype=BF, device="cuda")

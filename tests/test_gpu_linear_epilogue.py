@@ -12,6 +12,7 @@ import pytest
 import torch
 
 import fp8_quantized_lora_b200 as F
+from gpu_util import kernels_of
 from oracle import block
 
 pytestmark = pytest.mark.gpu
@@ -112,6 +113,64 @@ def test_nothing_in_the_epilogue_is_the_plain_forward(cuda_device, M, N, K):
                                    (128, 4096, 1024), (257, 1040, 4096), (1024, 2048, 2048)])
 def test_whole_numbers_are_exact(cuda_device, M, N, K):
     """Codes of -2 .. 2: Z is a whole number below 2^24, so Y is its rounding whatever the order of the sums."""
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    v = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float()  # noqa: E731
+    x, w, bias, res = v(M, K), v(N, K), v(N), v(M, N).to(BF)
+    one = torch.ones(1, device="cuda")
+    xq, wq = (t.to(torch.float8_e4m3fn).view(torch.uint8) for t in (x, w))
+    for which in (0, 1):
+        y, z = F.falqon_linear_fwd_epilogue(xq, one, wq, one, bias, which, res, z=True)
+        Z = x.double() @ w.double().T + bias
+        Y = (Z.clamp_min(0) if which else Z) + res
+        assert torch.equal(z, Z.to(F32).to(BF)) and torch.equal(y, Y.to(F32).to(BF))
+
+
+# Products that the rule leaves to 256 x 256 tiles on SM pairs (ragged rows, columns and K; a tile of 16 columns; more
+# tiles than pairs, whose rest runs whole or, at 4736 x 1280 and 2304 x 2064, in halves), few-row plans of 128 rows a
+# tile, which 64-row tiles are more than two an SM for, in more than one wave, and the largest plan of 64 rows (296
+# tiles; 297 at 19000 rows).
+PAIR, FEW128, FEW64 = "tc_gemm_pair_kernel", "6FewCfgILi128E", "6FewCfgILi64E"
+TILED = [(PAIR, 2048, 1296, 512), (PAIR, 4736, 1280, 256), (PAIR, 4700, 1296, 272), (PAIR, 2304, 2064, 1040),
+         (PAIR, 700, 2064, 8192), (FEW128, 300, 11008, 128), (FEW128, 20000, 128, 512), (FEW128, 19000, 128, 272),
+         (FEW64, 18900, 128, 272)]
+
+
+@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("kernel,M,N,K", TILED)
+def test_forward_of_each_kernel(cuda_device, kernel, M, N, K, which):
+    """test_forward's checks where the rule takes the kernel named."""
+    g = torch.Generator(device="cuda").manual_seed(M * 7 + N + which)
+    xq, s_x = _codes(g, (M, K), 1.0)
+    wq, s_w = _codes(g, (N, K), 0.1)
+    res = torch.randn(M, N, generator=g, device="cuda").to(BF)
+    ybuf, zbuf = (torch.full((M + 2, N), 7.0, dtype=BF, device="cuda") for _ in range(2))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for dtype in (BF, F32):
+        bias = torch.randn(N, generator=g, device="cuda").to(dtype)
+        ybuf[:M], zbuf[:M] = math.nan, math.nan
+
+        def call():
+            return F.falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias, which, res, z=zbuf[:M], y=ybuf[:M],
+                                                dev_status=st)
+        y, z = call()
+        assert int(st.item()) == 0
+        _check_fwd(xq, s_x, wq, s_w, bias, which, res, y, z)
+        assert (ybuf[M:] == 7.0).all() and (zbuf[M:] == 7.0).all()
+        launched = kernels_of(call)
+        assert len(launched) == 1 and kernel in launched[0][0], launched
+    # without the residual or Z, and the activation alone
+    y, none = F.falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias, which)
+    assert none is None
+    _check_fwd(xq, s_x, wq, s_w, bias, which, None, y, None)
+    y, _ = F.falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, act=which)
+    _check_fwd(xq, s_x, wq, s_w, None, which, None, y, None)
+    y, z = F.falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, act=which, residual=res, z=True)
+    _check_fwd(xq, s_x, wq, s_w, None, which, res, y, z)
+
+
+@pytest.mark.parametrize("kernel,M,N,K", TILED)
+def test_whole_numbers_are_exact_in_each_kernel(cuda_device, kernel, M, N, K):
+    """test_whole_numbers_are_exact's checks where the rule takes the kernel named."""
     g = torch.Generator(device="cuda").manual_seed(N + K)
     v = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float()  # noqa: E731
     x, w, bias, res = v(M, K), v(N, K), v(N), v(M, N).to(BF)

@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import fp8_quantized_lora_b200 as F
+from gpu_util import kernels_of
 from oracle import block
 
 pytestmark = pytest.mark.gpu
@@ -73,6 +74,30 @@ def test_forward(cuda_device, rows, cols, dtype, pdtype, rms):
     assert (mean is None) == rms
     _check_fwd(x, gamma, beta, 1e-5, rms, y, mean, rstd)
     assert (buf[rows:] == 7.0).all() and int(st.item()) == 0
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("dtype,pdtype", [(BF, F32), (F32, BF)])
+@pytest.mark.parametrize("rows,cols", [(10000, 24), (10000, 250), (10000, 400), (10001, 505), (10000, 515),
+                                       (5000, 700), (5000, 1003), (5000, 1280), (5003, 1801), (3000, 2056),
+                                       (3000, 3001), (3000, 4096), (1500, 8192), (1500, 8195), (600, 12001),
+                                       (600, 16384)])
+def test_forward_of_more_rows_than_fit(cuda_device, rows, cols, dtype, pdtype, rms):
+    """Every block (or warp) takes several rows, the next one read ahead, in each class of row lengths."""
+    x, gamma, beta, _, _ = _make(rows + cols, rows, cols, dtype, pdtype, True, rms)
+    buf = torch.full((rows + 2, cols), 7.0, dtype=dtype, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kind = F.NORM_RMS if rms else F.NORM_LAYER
+
+    def call():
+        return F.falqon_norm_fwd(x, gamma, beta, 1e-5, kind, y=buf[:rows], dev_status=st)
+    y, mean, rstd = call()
+    _check_fwd(x, gamma, beta, 1e-5, rms, y, mean, rstd)
+    assert (buf[rows:] == 7.0).all() and int(st.item()) == 0
+    (name, grid, block), = kernels_of(call)
+    assert "norm_fwd_row_kernel" in name
+    held = grid[0] * (block[0] // 32 if cols <= 505 else 1)  # a warp or a block a row
+    assert rows > held, (grid, block)
 
 
 @pytest.mark.parametrize("rms", [False, True])
