@@ -38,11 +38,13 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
-// z held to [-bound, bound]; NaN for NaN.
-__device__ __forceinline__ float clamp_nan(float z, float bound) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(z), "f"(bound));
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(y), "f"(-bound));
+// Two values held to [-bound, bound]; NaN for NaN.
+__device__ __forceinline__ float2 clamp2(float2 z, float bound) {
+  float2 y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y.x) : "f"(z.x), "f"(bound));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y.y) : "f"(z.y), "f"(bound));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y.x) : "f"(y.x), "f"(-bound));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y.y) : "f"(y.y), "f"(-bound));
   return y;
 }
 
@@ -107,24 +109,30 @@ __device__ __forceinline__ float2 logistic_slope2(float2 n, float2 zu) {
   return mul2(p, fma2(zu, fma2(p, both(-1.0f), both(1.0f)), both(1.0f)));
 }
 
+// Past some |z| a slope is 0 or 1 in float32 whatever z: z is held there, so
+// that no product of the largest z overflows or meets a factor of 0 as an
+// infinity.  The kept bf16 Z of a float32 bias of the lowest value, a mask, is
+// -infinity; its slope is 0.  (NaN stays NaN.)
 template <int kAct>
 __device__ __forceinline__ float2 act_slope2(float2 z) {
   if constexpr (kAct == FALQON_ACT_RELU) return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
   if constexpr (kAct == FALQON_ACT_GELU_ERF) {
+    z = clamp2(z, 20.0f);
     const float2 q = mul2(mul2(z, z), both(-0.5f * kLog2E));
     const float2 e = make_float2(exp2_fast(q.x), exp2_fast(q.y));
     const float2 h = mul2(normal_tail2(z), e);
     return fma2(mul2(z, both(kInvSqrt2Pi)), e, make_float2(normal_cdf(z.x, h.x), normal_cdf(z.y, h.y)));
   }
   if constexpr (kAct == FALQON_ACT_GELU_TANH) {
-    // past |z| = 20 p is 0 or 1 in float32 whatever z, and so is the slope:
-    // clamped there, no product overflows up to the largest z (NaN stays NaN)
-    z = make_float2(clamp_nan(z.x, 20.0f), clamp_nan(z.y, 20.0f));
+    z = clamp2(z, 20.0f);
     const float2 z2 = mul2(z, z);
     const float2 n = mul2(z, fma2(z2, both(-kGeluTwoU * kLog2E * kGeluCubic), both(-kGeluTwoU * kLog2E)));
     return logistic_slope2(n, mul2(z, fma2(z2, both(3.0f * kGeluTwoU * kGeluCubic), both(kGeluTwoU))));
   }
-  if constexpr (kAct == FALQON_ACT_SILU) return logistic_slope2(mul2(z, both(-kLog2E)), z);
+  if constexpr (kAct == FALQON_ACT_SILU) {
+    z = clamp2(z, 100.0f);
+    return logistic_slope2(mul2(z, both(-kLog2E)), z);
+  }
   return both(1.0f);
 }
 

@@ -266,6 +266,30 @@ def test_backward_up_to_the_largest_pre_activation(cuda_device, which):
         assert torch.isnan(dz[3, 5]) and torch.isnan(dbias[5]) and int(torch.isnan(dz).sum()) == 1
 
 
+@pytest.mark.parametrize("which", range(1, 5))
+@pytest.mark.parametrize("M", [3, 2304])
+def test_columns_masked_by_the_lowest_bias(cuda_device, M, which):
+    """A float32 bias of its type's lowest value switches a column off: y is 0 there, the bf16 Z that is kept is
+    -infinity (the lowest float32 is past bf16's by 3/4 of a step), and the gradient is 0, not NaN.  The greatest is
+    +infinity with slope 1."""
+    g = torch.Generator(device="cuda").manual_seed(which)
+    N, K = 272, 64
+    (xq, s_x), (wq, s_w) = _codes(g, (M, K), 1.0), _codes(g, (N, K), 0.1)
+    bias = torch.randn(N, generator=g, device="cuda")
+    off, on = torch.arange(0, N, 5, device="cuda"), torch.arange(1, N, 5, device="cuda")
+    bias[off], bias[on] = torch.finfo(F32).min, torch.finfo(F32).max
+    y, z = F.falqon_linear_fwd_epilogue(xq, s_x, wq, s_w, bias, which, z=True)
+    assert (y[:, off] == 0).all() and (z[:, off] == -math.inf).all() and (z[:, on] == math.inf).all()
+    rest = torch.ones(N, dtype=torch.bool, device="cuda")
+    rest[off] = rest[on] = False
+    dy = torch.full((M, N), 2.0 ** -6, dtype=BF, device="cuda")
+    dz, dbias = F.falqon_linear_epilogue_bwd(dy, z, which)
+    assert (dz[:, off] == 0).all() and (dbias[off] == 0).all()
+    assert torch.equal(dz[:, on], dy[:, on]) and (dbias[on] == M * 2.0 ** -6).all()
+    zr, dyr = z[:, rest], dy[:, rest]
+    _check_bwd(dyr, zr, which, dz[:, rest], dbias[rest])
+
+
 def test_gradient_against_differences(cuda_device):
     """The slope that the backward applies against differences of the forward's own activation: N(0, 1)
     pre-activations, one sample per element.  The forward's outputs are bf16, so the differences are taken of the
