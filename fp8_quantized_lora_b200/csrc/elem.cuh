@@ -103,14 +103,6 @@ __device__ __forceinline__ Words<kBytes> load_words(const void* p) {
   return r;
 }
 
-template <int kBytes>
-__device__ __forceinline__ void store_words(void* p, const Words<kBytes>& r) {
-  if constexpr (kBytes == 16) *static_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-  else if constexpr (kBytes == 8) *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
-  else if constexpr (kBytes == 4) *static_cast<uint32_t*>(p) = r.w[0];
-  else *static_cast<uint16_t*>(p) = static_cast<uint16_t>(r.w[0]);
-}
-
 // Values in kBytes of bf16 or float32.
 template <bool kBF16, int kBytes>
 constexpr int kValues = kBytes / (kBF16 ? 2 : 4);
@@ -122,18 +114,6 @@ __device__ __forceinline__ void values_of(const Words<kBytes>& r, float (&v)[kVa
     if constexpr (!kBF16) v[j] = __uint_as_float(r.w[j]);
     else v[j] = __uint_as_float(j & 1 ? r.w[j / 2] & 0xFFFF0000u : r.w[j / 2] << 16);
   }
-}
-
-template <bool kBF16, int kBytes>
-__device__ __forceinline__ Words<kBytes> words_of(const float (&v)[kValues<kBF16, kBytes>]) {
-  Words<kBytes> r;
-#pragma unroll
-  for (int j = 0; j < Words<kBytes>::N; ++j) {
-    if constexpr (!kBF16) r.w[j] = __float_as_uint(v[j]);
-    else if constexpr (kBytes == 2) r.w[j] = pack2(v[0], 0.0f);
-    else r.w[j] = pack2(v[2 * j], v[2 * j + 1]);
-  }
-  return r;
 }
 
 template <bool kBF16>

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(C::Threads, C::MinBlocks)
   const int tile = static_cast<int>(blockIdx.x) / g.splits;
   const int n0 = tile % g.n_tiles * kBM, m0 = tile / g.n_tiles * C::T;
   const int kb0 = split * g.kb_per_split;
-  const int nkb = max(0, min(g.kb_total, kb0 + g.kb_per_split) - kb0);
+  const int nkb = min(g.kb_total, kb0 + g.kb_per_split) - kb0;  // no split is empty (few_split)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::Stages; ++s) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(C::Threads, C::MinBlocks)
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          red[(c * 16 + j) * C::RedStride + q * 32 + lane] = nkb > 0 ? __uint_as_float(r[j]) : 0.0f;
+          red[(c * 16 + j) * C::RedStride + q * 32 + lane] = __uint_as_float(r[j]);
       }
     } else if (lane == 0) {
       fail();

@@ -19,8 +19,9 @@
 //               even CTA's full barrier, which the even producer arms.
 //   warp 1      TMEM allocation (both CTAs, together); in the even CTA the
 //               UMMA issuer (one lane).
-//   warps 2-5   epilogue: this CTA's 128 rows of the accumulator, scaled, bf16.
-//   warp 6      even CTA: MMA waiter.  It does the mbarrier waits and releases
+//   warps 2-5   epilogue: this CTA's 128 rows of the accumulator, scaled, bf16
+//               (kEpi: warps 2-9).
+//   warp 6      (kEpi: 10) even CTA: MMA waiter.  It does the mbarrier waits and releases
 //               the issuer through a named barrier (an mbarrier wait in the
 //               issuing thread would hold back its MMA stream).
 // The issuer's commits arrive on the barrier at the same offset in both

@@ -133,8 +133,7 @@ struct Unit {
   uint4 q;
 
   __device__ static __forceinline__ int column(int unit, int shift) { return unit * V - (kShift ? shift : 0); }
-  // whether any / every column of the unit at c exists
-  __device__ static __forceinline__ bool some(int c, int cols) { return c < cols; }
+  // whether every column of the unit at c exists (some do where c < cols)
   __device__ static __forceinline__ bool whole(int c, int cols) { return !kShift || (c >= 0 && c + V <= cols); }
   __device__ static __forceinline__ bool has(int c, int j, int cols) { return !kShift || (c + j >= 0 && c + j < cols); }
 

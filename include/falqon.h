@@ -582,8 +582,10 @@ FALQON_API const char* falqon_version(void);
  *  workspace (dgamma or dbeta wanted): falqon_workspace_size(
  *  FALQON_OP_NORM_BWD, rows, 0, cols, 0) bytes.
  *  Requirements: rows, cols >= 1 and below 2^31 - 256; cols need not be a
- *  multiple of anything (multiples of 8, 4 in float32, move in 16-byte
- *  vectors).
+ *  multiple of anything.  Up to 16384 columns (16377 in bfloat16, 16381 in
+ *  float32, where cols is no multiple of 8 or 4) a row is read once, in 16-byte
+ *  units; longer rows are read element by element, three times forward and
+ *  twice backward, with the sums over rows in the workspace.
  *  Device status (forward): NONFINITE when a row's statistics are not finite
  *  (an infinity or NaN in it, or squares past float32) or its rstd is 0 or
  *  infinite (eps = 0 on a constant row).  Device status (backward, dx wanted):
@@ -629,7 +631,9 @@ FALQON_API falqon_status falqon_linear_fwd_epilogue(const uint8_t* xq, const flo
  * output gradient; the residual's gradient is dY itself.
  *
  *  dy [M, N] bfloat16; z [M, N] bfloat16 as the forward kept it (may be NULL
- *  for FALQON_ACT_NONE, whose dZ is dY).
+ *  for FALQON_ACT_NONE, whose dZ is dY).  act' at an infinite Z (a Z past
+ *  bfloat16, such as a float32 bias of the lowest value leaves) is its limit,
+ *  0 or 1.
  *  dz [M, N] bfloat16, dbias [N] float32: each nullable, at least one wanted.
  *  workspace (dbias wanted): falqon_workspace_size(
  *  FALQON_OP_LINEAR_EPILOGUE_BWD, M, N, 0, 0) bytes.
