@@ -605,13 +605,17 @@ falqon_status clip_overlaps(int n, const void* const* grads, const falqon_dtype*
 // output, nor be the same.
 bool clip_results_overlap(int n, const void* const* grads, const falqon_dtype* dtypes, const int64_t* numel,
                           void* const* outs, const float* norm, const float* coef) {
-  const Bytes results[2] = {{norm, sizeof(float)}, {coef, sizeof(float)}};
-  if (overlap(results[0], results[1])) return true;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(norm), b = reinterpret_cast<uintptr_t>(coef ? coef : norm);
+  // the float at p meets [q, q + bytes): q - 3 <= p < q + bytes in one comparison
+  auto meets = [](uintptr_t p, const void* q, size_t bytes) {
+    return p + 3 - reinterpret_cast<uintptr_t>(q) < bytes + 3;
+  };
+  if (coef && meets(a, coef, sizeof(float))) return true;
   for (int i = 0; i < n; ++i) {
     if (numel[i] == 0) continue;
     const size_t bytes = bytes_of(dtypes[i], numel[i]);
-    for (const Bytes& r : results)
-      if (overlap(r, {grads[i], bytes}) || (outs && overlap(r, {outs[i], bytes}))) return true;
+    if (meets(a, grads[i], bytes) || meets(b, grads[i], bytes)) return true;
+    if (outs && (meets(a, outs[i], bytes) || meets(b, outs[i], bytes))) return true;
   }
   return false;
 }
