@@ -15,7 +15,7 @@
 // t = 1 / (1 + 0.44 |z| / sqrt 2) and P of degree 7, fitted here by iterated
 // least squares to erfc(x) exp(x^2) on 0 <= x <= 14 (relative error below
 // 2e-7), so the tail keeps its relative accuracy; erfcf took 45.5 us where
-// this took 28.2 us (backward, 4096 x 4096; 20 us with two values an
+// this took 28.2 us (backward, 4096 x 4096; 20.4 us with two values an
 // instruction).
 #pragma once
 

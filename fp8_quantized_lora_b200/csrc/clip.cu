@@ -43,8 +43,8 @@ constexpr int kClipFew = 32;        // the table of a launch of few tensors: its
 constexpr int kClipMany = 5, kClipFewer = 4, kClipSms = 148;
 constexpr int kClipBlocks = kClipMany * kClipSms;
 // The last chunks of a block's run that the norm leaves in the L2 for the
-// scaling, 6 x 740 x 16 KB = 73 MB in all; what it reads before them gives way
-// first (with the fifth block, 448 tensors of rank 64: 172 -> 160 us).
+// scaling, 6 x 740 x 16 KB = 73 MB in all, of which it then finds 57 to 59;
+// what it reads before them gives way first (with the fifth block, 448 tensors of rank 64: 172 -> 160 us).
 constexpr uint32_t kClipKeep = 6;
 
 template <int kTensors>

@@ -14,7 +14,7 @@
 // schedule.
 //
 // Measured on a B200 (us; in brackets the floor at 6.55 TB/s), GELU: 8192 x
-// 11008 86.5 (82.6), 4096 x 4096 19.5 to 20 (15.4); SiLU, 200 x 272: 3.2 (0.05;
+// 11008 86.7 (82.6), 4096 x 4096 19.8 (tanh), 20.4 (erf) (15.4); SiLU, 200 x 272: 3.2 (0.05;
 // two launches).
 #include "act.cuh"
 #include "elem.cuh"

@@ -19,10 +19,10 @@
 //   forward   4096 x 4096 bf16   RMS 12.8, layer 14.7 (10.2)
 //             4096 x 4096 fp32   RMS 23.4, layer 24.4 (20.5)
 //             8192 x 1537 bf16   RMS 12.1, layer 18.7 (7.7)
-//   backward  8192 x 4096 bf16 + dres   RMS 44.9, layer 47.8 (41.0)
-//             4096 x 4096 bf16   RMS 21.4, layer 25.2 (15.4)
-//             4096 x 4096 fp32   RMS 34.2, layer 36.9 (30.7)
-//             8192 x 1537 bf16   RMS 24.3, layer 33.6 (11.5)
+//   backward  8192 x 4096 bf16 + dres   RMS 44.9, layer 48.0 (41.0)
+//             4096 x 4096 bf16   RMS 21.4, layer 25.4 (15.4)
+//             4096 x 4096 fp32   RMS 34.4, layer 36.9 (30.7)
+//             8192 x 1537 bf16   RMS 24.9, layer 33.6 (11.5)
 //              300 x 4096 bf16   RMS 6.0, layer 7.3 (1.1)
 // (the backward with its second kernel, which joins the blocks' sums over the
 // rows: about 2.5 us).  float32 is near its bound; in bf16 the backward's
@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
       }
       // dx = g rs + xh a + b: the factors are of the size of the formula's own
       // terms.  (x - mu) times c2 rs^2 would spare RMS norms a product, but
-      // rs^2 leaves float32 where rs is 1e-19 or 1e19; times are within 2 %.
+      // rs^2 leaves float32 where rs is 1e-19 or 1e19; times are within 4 %.
       const float a = -c2 * inv * rs, b = -c1 * inv * rs;
       // a NaN or infinity in the row or its statistics, or sums past float32
       if (t == 0 && dev_status && !isfinite(a + b)) atomicOr(dev_status, kDevNonfinite);
