@@ -588,8 +588,9 @@ FALQON_API const char* falqon_version(void);
  *  twice backward, with the sums over rows in the workspace.
  *  Device status (forward): NONFINITE when a row's statistics are not finite
  *  (an infinity or NaN in it, or squares past float32) or its rstd is 0 or
- *  infinite (eps = 0 on a constant row, or one whose squares vanish in float32).  Device status (backward, dx wanted):
- *  NONFINITE when a row's c1, c2 or rstd make its dx infinite or NaN.
+ *  infinite (eps = 0 on a constant row, or one whose squares vanish in
+ *  float32).  Device status (backward, dx wanted): NONFINITE when a row's c1, c2
+ *  or rstd make its dx infinite or NaN.
  */
 FALQON_API falqon_status falqon_norm_fwd(const void* x, falqon_dtype dtype, const void* gamma, const void* beta,
                                          falqon_dtype param_dtype, falqon_norm kind, int64_t rows, int64_t cols,
